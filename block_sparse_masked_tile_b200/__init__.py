@@ -18,6 +18,8 @@ The API follows the tensorplay.nn.attention page:
 * Mask builders: ``noop_mask``, ``causal``, ``sliding_window``,
   ``prefix_lm``, ``sink``, ``document``, ``and_masks`` and ``or_masks``.
 * Score mods: ``softcap`` and ``alibi``.
+* Positions and serving (``serving.py``): ``rotary``, a paged cache in 8 bits
+  (``create_paged_cache``, ``cache_*``) and ``paged_attention`` over it.
 """
 from __future__ import annotations
 
@@ -34,6 +36,10 @@ __all__ = [
     "check_device_status", "library_path", "mask_from_tree", "score_mods_from_list", "splitkv_workspace_bytes",
     "flex_attention_host", "host_workspace_bytes", "flex_attention_varlen", "seqlens_to_doc_ids", "flex_attention_backward",
     "backward_workspace_bytes", "flex_attention_varlen_backward",
+    # serving.py
+    "RotarySpec", "rotary_spec", "rotary", "rotary_backward", "PagedCache", "create_paged_cache", "cache_extend",
+    "cache_write", "cache_gather", "cache_fork", "cache_free", "cache_compact", "cache_workspace_bytes",
+    "paged_attention", "paged_attention_workspace_bytes",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -46,7 +52,7 @@ MAX_SCORE_OPS = 2
 SCORE_NONE, SCORE_SOFTCAP, SCORE_ALIBI = 0, 1, 2
 STATUS_NAMES = {
     0: "OK", 1: "INVALID_ARGUMENT", 2: "SHAPE_MISMATCH", 3: "UNSUPPORTED", 4: "CUDA_ERROR",
-    5: "DEVICE_TIMEOUT", 6: "DEVICE_BOUNDS", 7: "DEVICE_PRECONDITION",
+    5: "DEVICE_TIMEOUT", 6: "DEVICE_BOUNDS", 7: "DEVICE_PRECONDITION", 8: "DEVICE_CAPACITY",
 }
 
 
@@ -969,3 +975,9 @@ def check_device_status(device=None) -> None:
     device = torch.device("cuda") if device is None else torch.device(device)
     with torch.cuda.device(device):
         _check(_lib.bsmt_check_device_status(ctypes.c_void_p(_stream_ptr(device))))
+
+
+from .serving import (  # noqa: E402  (it takes the library and the mask types from above)
+    PagedCache, RotarySpec, cache_compact, cache_extend, cache_fork, cache_free, cache_gather, cache_workspace_bytes,
+    cache_write, create_paged_cache, paged_attention, paged_attention_workspace_bytes, rotary, rotary_backward,
+    rotary_spec)

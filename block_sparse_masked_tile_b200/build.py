@@ -17,8 +17,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbsmt.so")
-SOURCES = ["bsmt.cu"]
-HEADERS = sorted(f for f in os.listdir(CSRC) if f.endswith(".cuh"))
+SOURCES = ["bsmt.cu", "serving.cu"]
+HEADERS = sorted(f for f in os.listdir(CSRC) if f.endswith((".cuh", ".h")))
 
 
 def nvcc() -> str:
@@ -32,27 +32,41 @@ def needs_build() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, "bsmt.h"), __file__]
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] + [__file__]
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 
 def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     if not force and not needs_build():
         return LIB
-    cmd = [
-        nvcc(), "-shared", "-Xcompiler", "-fPIC", "-std=c++17", "-O3", "-lineinfo",
-        "-gencode", "arch=compute_100a,code=sm_100a",
-        "--expt-relaxed-constexpr",
-        "-I", INCLUDE, "-I", CSRC,
-        "-o", LIB + ".tmp",
-    ] + [os.path.join(CSRC, f) for f in SOURCES] + ["-lcudart"]
-    cmd[1:1] = ["-Xptxas", "-v"]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if ptxas_verbose or res.returncode != 0:
-        sys.stderr.write(res.stderr)
+    # one nvcc for each source, side by side; the objects are linked into the library
+    jobs = []
+    for f in SOURCES:
+        obj = os.path.join(CSRC, os.path.splitext(f)[0] + ".o")
+        cmd = [
+            nvcc(), "-c", "-Xptxas", "-v", "-Xcompiler", "-fPIC", "-std=c++17", "-O3", "-lineinfo",
+            "-gencode", "arch=compute_100a,code=sm_100a",
+            "--expt-relaxed-constexpr",
+            "-I", INCLUDE, "-I", CSRC,
+            "-o", obj, os.path.join(CSRC, f),
+        ]
+        jobs.append((f, obj, subprocess.Popen(cmd, stderr=subprocess.PIPE, stdout=subprocess.DEVNULL, text=True)))
+    logs = {f: job.communicate()[1] for f, _, job in jobs}
+    failed = [f for f, _, job in jobs if job.returncode != 0]
+    for f, log in logs.items():
+        if ptxas_verbose or f in failed:
+            sys.stderr.write(log)
+    if failed:
+        raise RuntimeError(f"nvcc failed on {', '.join(failed)}")
+    check_attention_registers(logs["bsmt.cu"])
+    link = [nvcc(), "-shared", "-gencode", "arch=compute_100a,code=sm_100a", "-o", LIB + ".tmp",
+            *(obj for _, obj, _ in jobs), "-lcudart"]
+    res = subprocess.run(link, capture_output=True, text=True)
+    for _, obj, _ in jobs:
+        os.remove(obj)
     if res.returncode != 0:
-        raise RuntimeError("nvcc failed")
-    check_attention_registers(res.stderr)
+        sys.stderr.write(res.stderr)
+        raise RuntimeError("linking failed")
     os.replace(LIB + ".tmp", LIB)
     return LIB
 

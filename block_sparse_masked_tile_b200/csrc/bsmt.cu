@@ -19,6 +19,7 @@
 #include "attn_bwd.cuh"
 #include "attn_fwd.cuh"
 #include "bsmt.h"
+#include "host_common.h"
 #include "mask_build.cuh"
 #include "mask_transpose.cuh"
 #include "varlen.cuh"
@@ -320,15 +321,8 @@ __global__ void fill_empty_kernel(uint4* out, int64_t out_vec, float* lse, int64
         lse[i] = -INFINITY;
 }
 
-// Score mods -> compile-time mode (kScore*), the soft-cap and the ALiBi slopes
-// (explicit, or the default ones of heads h0 .. h0 + Hq - 1 of a model of
-// `heads` heads).
-struct ScoreArgs {
-    int mode = bsmt::kScoreNone;
-    float cap = 1.f;
-    const float* slopes = nullptr;
-    int32_t alibi_h0 = 0, alibi_heads = 1;
-};
+// Score mods -> compile-time mode (kScore*), the soft-cap and the ALiBi slopes.
+using bsmt_host::ScoreArgs;
 
 bsmt_status parse_score(const bsmt_score_spec* score, int64_t Hq, ScoreArgs* out_args) {
     int mode = bsmt::kScoreNone;
@@ -757,8 +751,9 @@ bsmt_status bsmt_check_device_status(void* stream) {
         const int zero = 0;
         cudaMemcpyToSymbol(bsmt::g_status, &zero, sizeof(int));
         const char* what = v == BSMT_ERR_DEVICE_TIMEOUT     ? "a pipeline wait ran out of time"
-                           : v == BSMT_ERR_DEVICE_BOUNDS    ? "a block index outside [0, KB) or a bad count"
-                           : v == BSMT_ERR_DEVICE_PRECONDITION ? "kv document ids are not non-decreasing"
+                           : v == BSMT_ERR_DEVICE_BOUNDS    ? "a block index outside [0, KB) or a bad count; or a cache's sequence, position or page out of range"
+                           : v == BSMT_ERR_DEVICE_PRECONDITION ? "kv document ids are not non-decreasing; or a cache call whose lists or pages do not meet its conditions"
+                           : v == BSMT_ERR_DEVICE_CAPACITY     ? "a cache has too few free pages, or a sequence too few places"
                                                             : "unknown device error";
         return fail(static_cast<bsmt_status>(v), "device status %d: %s", v, what);
     }
@@ -1476,3 +1471,40 @@ extern "C" bsmt_status bsmt_flex_attention_host(const void* q, const void* k, co
     if (ce != cudaSuccess) return fail(BSMT_ERR_CUDA, "host pipeline: %s", cudaGetErrorString(ce));
     return ok();
 }
+
+// ------------------------------------------- for the other translation units
+namespace bsmt_host {
+
+bsmt_status fail(bsmt_status code, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof(buf), fmt, ap);
+    va_end(ap);
+    g_last_error = buf;
+    return code;
+}
+
+bsmt_status ok() { return ::ok(); }
+
+bsmt_status build_dnf(const bsmt_mask_spec* spec, int64_t B, bsmt::MaskDnf* out) { return ::build_dnf(spec, B, out); }
+
+bsmt_status score_args(const bsmt_score_spec* score, int64_t Hq, ScoreArgs* out) { return ::parse_score(score, Hq, out); }
+
+bsmt_status sm_count(int* dev, int* n) { return ::sm_count(dev, n); }
+
+bsmt_status status_word(int dev, int** addr) {
+    static void* kept[64] = {};
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (kept[dev] == nullptr) {
+        void* ptr = nullptr;
+        const cudaError_t e = cudaGetSymbolAddress(&ptr, bsmt::g_status);
+        if (e != cudaSuccess || ptr == nullptr)
+            return ::fail(BSMT_ERR_CUDA, "cudaGetSymbolAddress(status word): %s", cudaGetErrorString(e));
+        kept[dev] = ptr;
+    }
+    *addr = static_cast<int*>(kept[dev]);
+    return BSMT_OK;
+}
+
+}  // namespace bsmt_host

@@ -1,0 +1,868 @@
+// Attention of the newest tokens of many sequences over the 8-bit paged cache.
+//
+//   out = softmax_j(mod(scale * q . k_j), masked) v,  k_j = code * k_scale[page, head]
+//
+// A unit is (sequence, row tile, kv head): a row is one query token with one
+// query head of the kv head's group, a row tile 16 * RT of them. A unit's keys
+// are cut into tiles of 32 tokens; tiles that no row sees are never read. All
+// units' tiles form one list that is cut into equal shares, one for each block,
+// so sequences of any lengths keep all blocks busy to the end. A unit that a
+// share boundary cuts leaves parts (O, the running maxima and the sum, in fp32)
+// in the workspace, which paged_combine_kernel joins in a fixed order.
+//
+// Bound by HBM: K and V codes are read once. Each warp of a block takes every
+// fourth tile of the share and has its own pipeline of cp.async stages. Which
+// bytes of a tile a lane copies is chosen so that it is the lane that uses them:
+// the contraction's order is free, so a lane's 16 bytes of a K row are the four
+// k positions of four MMA steps, and its 16 bytes of a V row are one column of 16
+// output tiles. No barrier, shared-memory transpose or bank conflict comes in.
+//
+// Codes become halves exactly (e4m3 by cvt, int8 by byte permutes); q, scaled by
+// a power of two for each row, becomes halves exactly down to 2^-28 of the row's
+// largest value. The matrix unit is mma.sync m16n8k16 with fp32 accumulation:
+// eight or sixteen rows against a tile are some 5% of its rate here, and tcgen05
+// takes 8-bit operands only in pairs, which would round q and P to 8 bits.
+//
+// Softmax in base 2 with two running maxima for each row: m of the scores, for
+// the sum l, and mo of score + log2(v_scale), for O, so that P * v_scale, a half,
+// never exceeds 1 whatever the pages' scales are.
+#pragma once
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "kv_cache.cuh"
+#include "mask_dnf.cuh"
+
+namespace bsmt {
+
+constexpr int kPagedWarps = 4;
+constexpr int kPagedThreads = 32 * kPagedWarps;
+constexpr int kTileTokens = 32;
+
+struct PagedParams {
+    KvCache c;
+    const __nv_bfloat16* q;  // [T, Hq, D]
+    const int32_t* seqs;
+    const int32_t* cu;  // NULL: one token a sequence
+    __nv_bfloat16* out;
+    float* lse;       // [Hq, T]
+    float* part_o;    // [2 * blocks][16 * RT][D]
+    float* part_m;    // [2 * blocks][16 * RT][4]: m, mo, l
+    int32_t* heads_of_parts;  // [blocks][8]: a cut unit that begins in this block
+    const float* slopes;
+    int64_t T;
+    int32_t n, layer, Hq, group, min_share;
+    float scale, cap;
+    int32_t alibi, alibi_first, alibi_h0, alibi_heads, softcap;
+    int* status;
+};
+
+template <int D>
+struct PagedStage {
+    static constexpr int kK = kTileTokens * D, kV = kTileTokens * D;
+    static constexpr int kBytes = kK + kV + 16;  // and the page scales: k, k, v, v
+    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kWarpBytes = kStages * kBytes;
+    static constexpr int kSmem = kPagedWarps * kWarpBytes;
+};
+
+// Dynamic shared memory of one block: the stages and, for RT = 2, q's fragments.
+template <int D, int RT>
+constexpr int paged_smem() {
+    return PagedStage<D>::kSmem + (RT > 1 ? RT * (D / 16) * 512 : 0);
+}
+
+__device__ __forceinline__ uint32_t shared_addr(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool there) {
+    const uint32_t n = there ? BYTES : 0;  // 0: the destination is zeroed and src not read
+    if (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 r;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ float lds32f(uint32_t a) {
+    float r;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(a));
+    return r;
+}
+
+__device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Codes 0, 1 (LOW) or 2, 3 of a word as halves. The int8 codes come with their
+// top bit flipped (u = code + 128): the half 0x6400 | u is 1024 + u.
+template <bool INT8, bool LOW>
+__device__ __forceinline__ uint32_t halves_of(uint32_t w) {
+    if (INT8) {
+        const uint32_t x = __byte_perm(w, 0x64646464u, LOW ? 0x4140 : 0x4342);
+        const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0x6480)));
+        return *reinterpret_cast<const uint32_t*>(&y);
+    }
+    return e4m3x2_to_half2(LOW ? w & 0xFFFFu : w >> 16);
+}
+
+template <bool INT8>
+__device__ __forceinline__ uint32_t flip(uint32_t w) {
+    return INT8 ? w ^ 0x80808080u : w;
+}
+
+// The tiles that some query in [q_lo, q_hi] of a sequence of `len` tokens sees:
+// up to kMaxTerms disjoint runs, ascending. Returns the number of tiles.
+__device__ __forceinline__ int seen_tiles(const MaskDnf& dnf, int64_t q_lo, int64_t q_hi, int64_t len, int* first,
+                                          int* last, int* runs) {
+    int n = 0, total = 0;
+    for (int t = 0; t < dnf.n_terms; ++t) {
+        int64_t lo, hi, unused;
+        term_interval(dnf, t, q_lo, 0, len - 1, 0, 0, lo, unused);  // intervals move up with the query
+        term_interval(dnf, t, q_hi, 0, len - 1, 0, 0, unused, hi);
+        if (lo > hi) continue;
+        int a = static_cast<int>(lo / kTileTokens), b = static_cast<int>(hi / kTileTokens);
+        // into the sorted list, with every run that it meets
+        int at = 0, keep = 0;
+        int i = 0;
+        while (i < n && last[i] < a) ++i;
+        at = i;
+        while (i < n && first[i] <= b) {
+            a = min(a, first[i]);
+            b = max(b, last[i]);
+            total -= last[i] - first[i] + 1;
+            ++i;
+        }
+        keep = n - i;
+        if (i > at) {  // `i - at` runs become one
+            for (int j = 0; j < keep; ++j) first[at + 1 + j] = first[i + j], last[at + 1 + j] = last[i + j];
+        } else {
+            for (int j = keep; j > 0; --j) first[at + j] = first[at + j - 1], last[at + j] = last[at + j - 1];
+        }
+        first[at] = a;
+        last[at] = b;
+        total += b - a + 1;
+        n = at + 1 + keep;
+    }
+    *runs = n;
+    return total;
+}
+
+struct PagedSeq {
+    int slot;           // row of the page table, -1: none (length 0)
+    int64_t len;
+    int64_t q0;         // the first query token
+    int count;          // queries
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int i) {
+    PagedSeq s;
+    s.slot = __ldg(p.seqs + i);
+    int64_t q0 = i, q1 = i + 1;
+    if (p.cu != nullptr) {
+        q0 = __ldg(p.cu + i);
+        q1 = __ldg(p.cu + i + 1);
+        if (q0 < 0 || q1 < q0 || q1 > p.T) {
+            set_status(p.status, BSMT_ERR_DEVICE_PRECONDITION);
+            q1 = q0;
+        }
+    }
+    s.q0 = q0;
+    s.count = static_cast<int>(q1 - q0);
+    s.len = 0;
+    if (s.slot < 0 || s.slot >= p.c.max_seqs) {
+        if (s.slot != -1) set_status(p.status, BSMT_ERR_DEVICE_BOUNDS);
+        s.slot = -1;
+    } else {
+        const int64_t len = __ldg(p.c.seq_lens + s.slot);
+        if (len < 0 || len > seq_capacity(p.c))
+            set_status(p.status, BSMT_ERR_DEVICE_BOUNDS);
+        else
+            s.len = len;
+    }
+    return s;
+}
+
+// What the blocks need of the sequence that they work on.
+struct PagedSeqShared {
+    PagedSeq s;
+    int64_t weight;  // tiles of all its units
+    int tiles, row_tiles, runs;
+    int first[kMaxTerms], last[kMaxTerms];          // runs of seen tiles
+    int64_t clean_lo[kMaxTerms], clean_hi[kMaxTerms];  // keys that every query sees, for each term
+};
+
+// A sequence without a key still has one (empty) tile, which writes its rows.
+__device__ __forceinline__ int64_t paged_weight(const PagedParams& p, const PagedSeq& s, int tiles, int rows_of_tile) {
+    if (s.count == 0) return 0;
+    const int64_t row_tiles = (static_cast<int64_t>(s.count) * p.group + rows_of_tile - 1) / rows_of_tile;
+    return row_tiles * p.c.heads * max(tiles, 1);
+}
+
+template <int D, bool INT8, int RT, bool MODS>
+__global__ void __launch_bounds__(kPagedThreads, 2) paged_attention_kernel(const __grid_constant__ PagedParams p,
+                                                                           const __grid_constant__ MaskDnf dnf) {
+    using Stage = PagedStage<D>;
+    constexpr int kSteps = D / 16;   // MMA steps over the head dimension
+    constexpr int kChunks = D / 64;  // 16-byte pieces of a K row that one lane holds
+    constexpr int kOut = D / 8;      // output tiles of 8 columns
+    constexpr int kRows = 16 * RT;
+    constexpr float kLog2e = 1.4426950408889634f;
+    constexpr float kLn2 = 0.6931471805599453f;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ long long s_scan[kPagedWarps];
+    __shared__ long long s_off;
+    __shared__ int s_i;
+    __shared__ PagedSeqShared s_seq;
+    __shared__ float s_qscale[kRows];
+    const KvCache& c = p.c;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;
+
+    // ---- this block's share of all tiles
+    const int per_thread = (p.n + kPagedThreads - 1) / kPagedThreads;
+    const int i_lo = min(p.n, tid * per_thread), i_hi = min(p.n, i_lo + per_thread);
+    long long mine = 0;
+    for (int i = i_lo; i < i_hi; ++i) {
+        const PagedSeq s = paged_seq(p, i);
+        int first[kMaxTerms], last[kMaxTerms], runs;
+        const int tiles = seen_tiles(dnf, s.len - s.count, s.len - 1, s.len, first, last, &runs);
+        mine += paged_weight(p, s, tiles, kRows);
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+        if (lane >= d) incl += y;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    long long all = 0, before = incl - mine;
+#pragma unroll
+    for (int w = 0; w < kPagedWarps; ++w) {
+        all += s_scan[w];
+        if (w < warp) before += s_scan[w];
+    }
+    long long share = (all + gridDim.x - 1) / gridDim.x;
+    if (share < p.min_share) share = p.min_share;
+    const long long begin = share * blockIdx.x, end = min(all, begin + share);
+    if (begin < end && before <= begin && begin < before + mine) {
+        long long off = begin - before;
+        for (int i = i_lo; i < i_hi; ++i) {
+            const PagedSeq s = paged_seq(p, i);
+            int first[kMaxTerms], last[kMaxTerms], runs;
+            const int tiles = seen_tiles(dnf, s.len - s.count, s.len - 1, s.len, first, last, &runs);
+            const long long w = paged_weight(p, s, tiles, kRows);
+            if (off < w) {
+                s_i = i;
+                s_off = off;
+                break;
+            }
+            off -= w;
+        }
+    }
+    if (tid == 0) p.heads_of_parts[blockIdx.x * 8] = 0;
+    // rows behind the last sequence belong to none: they see nothing
+    if (p.cu != nullptr) {
+        const int64_t used = max(0, min(__ldg(p.cu + p.n), static_cast<int>(p.T)));
+        const int64_t stride = static_cast<int64_t>(gridDim.x) * kPagedThreads;
+        const int64_t rest = (p.T - used) * p.Hq;
+        uint4* o = reinterpret_cast<uint4*>(p.out + used * p.Hq * D);
+        for (int64_t x = static_cast<int64_t>(blockIdx.x) * kPagedThreads + tid; x < rest * (D / 8); x += stride)
+            o[x] = make_uint4(0, 0, 0, 0);
+        for (int64_t x = static_cast<int64_t>(blockIdx.x) * kPagedThreads + tid; x < rest; x += stride)
+            p.lse[x / (p.T - used) * p.T + used + x % (p.T - used)] = -INFINITY;
+    }
+    __syncthreads();
+    if (begin >= end) return;
+
+    int i = s_i;
+    long long off = s_off, left = end - begin;
+    bool first_segment = true;
+    const uint32_t stages = shared_addr(smem) + warp * Stage::kWarpBytes;
+    const int64_t head_bytes = static_cast<int64_t>(c.page) * D;
+    const int64_t page_bytes = head_bytes * c.heads;
+
+    for (; left > 0 && i < p.n; ++i, off = 0) {
+        __syncthreads();
+        if (tid == 0) {
+            const PagedSeq s = paged_seq(p, i);
+            s_seq.s = s;
+            s_seq.tiles = seen_tiles(dnf, s.len - s.count, s.len - 1, s.len, s_seq.first, s_seq.last, &s_seq.runs);
+            s_seq.weight = paged_weight(p, s, s_seq.tiles, kRows);
+            for (int x = 0; x < dnf.n_terms; ++x) {
+                int64_t unused;
+                term_interval(dnf, x, s.len - 1, 0, s.len - 1, 0, 0, s_seq.clean_lo[x], unused);
+                term_interval(dnf, x, s.len - s.count, 0, s.len - 1, 0, 0, unused, s_seq.clean_hi[x]);
+            }
+        }
+        __syncthreads();
+        const int64_t len = s_seq.s.len;
+        const int count = s_seq.s.count;
+        const int seen = s_seq.tiles, tiles = max(seen, 1);
+        const int64_t weight = s_seq.weight;
+        const int32_t* table = c.page_table + static_cast<int64_t>(max(s_seq.s.slot, 0)) * c.max_pages;
+
+        while (off < weight && left > 0) {
+            const int64_t unit = off / tiles;
+            const int t0 = static_cast<int>(off - unit * tiles);
+            const int t1 = static_cast<int>(min(static_cast<long long>(tiles), t0 + left));
+            const int head = static_cast<int>(unit % c.heads);
+            const int64_t row0 = unit / c.heads * kRows;  // the unit's first row
+            const int64_t rows_all = static_cast<int64_t>(count) * p.group;
+
+            // ---- pipeline over this warp's tiles
+            const uint8_t* k_head = c.k + static_cast<int64_t>(p.layer) * c.pages * page_bytes + head * head_bytes;
+            const uint8_t* v_head = c.v + static_cast<int64_t>(p.layer) * c.pages * page_bytes + head * head_bytes;
+            const float* k_scale = c.k_scale + static_cast<int64_t>(p.layer) * c.pages * c.heads + head;
+            const float* v_scale = c.v_scale + static_cast<int64_t>(p.layer) * c.pages * c.heads + head;
+            int run = 0, run_base = 0;  // the run that the next tile to load lies in, and the tiles before it
+            auto tile_of = [&](int ord) -> int64_t {  // first token of the unit's tile `ord`; -1: none
+                if (ord >= t1 || ord >= seen) return -1;
+                while (ord - run_base > s_seq.last[run] - s_seq.first[run]) {
+                    run_base += s_seq.last[run] - s_seq.first[run] + 1;
+                    ++run;
+                }
+                return static_cast<int64_t>(s_seq.first[run] + ord - run_base) * kTileTokens;
+            };
+            auto page_at = [&](int64_t tok) -> int {  // page of a token; -1: behind the sequence, or a bad one
+                if (tok < 0 || tok >= len) return -1;
+                return __ldg(table + (tok >> c.page_shift));
+            };
+            auto check_page = [&](int page) -> int {
+                if (page >= 0 && page < c.pages) return page;
+                return -1;
+            };
+            int next_ord = t0 + warp;
+            int64_t next_tok = tile_of(next_ord);
+            int next_a = page_at(next_tok), next_b = page_at(next_tok < 0 ? -1 : next_tok + 16);
+            auto issue = [&](int stage) {
+                const uint32_t st = stages + stage * Stage::kBytes;
+                if (next_tok >= 0) {
+                    const int pa = check_page(next_a), pb = check_page(next_b);
+                    if ((pa < 0 || (pb < 0 && next_tok + 16 < len)) && lane == 0)
+                        set_status(p.status, BSMT_ERR_DEVICE_BOUNDS);
+                    const int in_page = static_cast<int>(next_tok & (c.page - 1));
+                    const int in_b = static_cast<int>((next_tok + 16) & (c.page - 1));
+                    const int64_t base_a = pa < 0 ? 0 : pa * page_bytes + static_cast<int64_t>(in_page) * D;
+                    const int64_t base_b = pb < 0 ? 0 : pb * page_bytes + static_cast<int64_t>(in_b) * D;
+                    const int have = static_cast<int>(min(static_cast<int64_t>(kTileTokens), len - next_tok));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const bool there = 8 * j + g < have && (j < 2 ? pa : pb) >= 0;
+                        const uint8_t* src = k_head + (j < 2 ? base_a : base_b) + ((j & 1) * 8 + g) * D + 16 * t;
+#pragma unroll
+                        for (int x = 0; x < kChunks; ++x)
+                            cp_async<16>(st + (j * kChunks + x) * 512 + lane * 16, src + 64 * x, there);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int row = 2 * t + (x & 1) + 8 * (x >> 1);
+                            const bool there = 16 * h + row < have && (h ? pb : pa) >= 0;
+                            const uint8_t* src = v_head + (h ? base_b : base_a) + row * D + g * (D / 8);
+                            cp_async<D / 8>(st + Stage::kK + ((h * 4 + x) * 32 + lane) * (D / 8), src, there);
+                        }
+                    }
+                    if (lane < 4) {
+                        const int page = (lane & 1) ? pb : pa;
+                        const float* src = ((lane & 2) ? v_scale : k_scale) + static_cast<int64_t>(max(page, 0)) * c.heads;
+                        cp_async<4>(st + Stage::kK + Stage::kV + lane * 4, src, page >= 0);
+                    }
+                }
+                cp_async_commit();
+                next_ord += kPagedWarps;
+                next_tok = tile_of(next_ord);
+                next_a = page_at(next_tok);
+                next_b = page_at(next_tok < 0 ? -1 : next_tok + 16);
+            };
+            int64_t tok_q[Stage::kStages];  // first tokens of the tiles in flight
+#pragma unroll
+            for (int x = 0; x < Stage::kStages; ++x) {
+                tok_q[x] = next_tok;
+                issue(x);
+            }
+
+            // ---- q: rows g and g + 8 of each row tile, in halves
+            uint32_t qf[RT > 1 ? 1 : kSteps][4];
+            float qs[RT][2];
+            int64_t pos[RT][2];
+            float slope[RT][2];
+            bool valid[RT][2];
+            const uint32_t q_smem = shared_addr(smem) + Stage::kSmem;
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t row = row0 + 16 * r + 8 * h + g;
+                    valid[r][h] = row < rows_all;
+                    const int64_t qi = valid[r][h] ? row / p.group : 0;
+                    const int hq = head * p.group + static_cast<int>(valid[r][h] ? row - qi * p.group : 0);
+                    pos[r][h] = len - count + qi;
+                    slope[r][h] = 0.f;
+                    if (MODS && p.alibi)
+                        slope[r][h] = p.slopes != nullptr
+                                          ? __ldg(p.slopes + hq)
+                                          : exp2f(-8.f * static_cast<float>(p.alibi_h0 + hq + 1) / static_cast<float>(p.alibi_heads));
+                    uint32_t w[kChunks][8];
+                    const uint4* src = reinterpret_cast<const uint4*>(p.q + ((s_seq.s.q0 + qi) * p.Hq + hq) * D + 16 * t);
+#pragma unroll
+                    for (int x = 0; x < kChunks; ++x) {
+                        const uint4 a = valid[r][h] ? __ldg(src + 8 * x) : make_uint4(0, 0, 0, 0);
+                        const uint4 b = valid[r][h] ? __ldg(src + 8 * x + 1) : make_uint4(0, 0, 0, 0);
+                        w[x][0] = a.x, w[x][1] = a.y, w[x][2] = a.z, w[x][3] = a.w;
+                        w[x][4] = b.x, w[x][5] = b.y, w[x][6] = b.z, w[x][7] = b.w;
+                    }
+                    uint32_t most = 0;
+#pragma unroll
+                    for (int x = 0; x < kChunks; ++x)
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            const uint32_t a = w[x][y] & 0x7FFFu, b = w[x][y] >> 16 & 0x7FFFu;
+                            most = max(most, max(a < 0x7F80u ? a : 0u, b < 0x7F80u ? b : 0u));
+                        }
+                    most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+                    most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+                    // largest value to [2^14, 2^15): the row's small values keep their bits, too
+                    const int e = max(static_cast<int>(most >> 7) - 127, -100) - 14;
+                    qs[r][h] = exp2i(e) * p.scale * (MODS ? 1.f : kLog2e);
+                    const float up = exp2i(-e);
+#pragma unroll
+                    for (int x = 0; x < kChunks; ++x)
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            const __half2 v = __floats2half2_rn(__uint_as_float(w[x][y] << 16) * up,
+                                                                __uint_as_float(w[x][y] & 0xFFFF0000u) * up);
+                            const uint32_t u = *reinterpret_cast<const uint32_t*>(&v);
+                            // step 4 x + y / 2: a[0], a[1] rows g, g + 8 of the first pair, a[2], a[3] of the second
+                            if (RT == 1)
+                                qf[4 * x + y / 2][h + 2 * (y & 1)] = u;
+                            else if (warp == r)
+                                asm volatile("st.shared.u32 [%0], %1;" ::"r"(q_smem + ((r * kSteps + 4 * x + y / 2) * 32 + lane) * 16 +
+                                                                             (h + 2 * (y & 1)) * 4),
+                                             "r"(u)
+                                             : "memory");
+                        }
+                }
+            }
+            if (RT > 1) __syncthreads();
+
+            float o[RT][kOut][4];
+            float m[RT][2], mo[RT][2], l[RT][2];
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) m[r][h] = mo[r][h] = -INFINITY, l[r][h] = 0.f;
+#pragma unroll
+                for (int x = 0; x < kOut; ++x)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) o[r][x][y] = 0.f;
+            }
+
+            int stage = 0;
+            for (int ord = t0 + warp; ord < t1; ord += kPagedWarps) {
+                cp_async_wait<Stage::kStages - 1>();
+                __syncwarp();
+                const int64_t tok = tok_q[0];
+                const uint32_t st = stages + stage * Stage::kBytes;
+                if (tok >= 0) {
+                    float s[RT][4][4];
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) s[r][j][y] = 0.f;
+#pragma unroll
+                    for (int x = 0; x < kChunks; ++x) {
+                        uint4 kw[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) kw[j] = lds128(st + (j * kChunks + x) * 512 + lane * 16);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            uint32_t a[RT][4];
+#pragma unroll
+                            for (int r = 0; r < RT; ++r) {
+                                if (RT == 1) {
+#pragma unroll
+                                    for (int z = 0; z < 4; ++z) a[r][z] = qf[4 * x + y][z];
+                                } else {
+                                    const uint4 v = lds128(q_smem + ((r * kSteps + 4 * x + y) * 32 + lane) * 16);
+                                    a[r][0] = v.x, a[r][1] = v.y, a[r][2] = v.z, a[r][3] = v.w;
+                                }
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t w = flip<INT8>(y == 0 ? kw[j].x : y == 1 ? kw[j].y : y == 2 ? kw[j].z : kw[j].w);
+                                const uint32_t b0 = halves_of<INT8, true>(w), b1 = halves_of<INT8, false>(w);
+#pragma unroll
+                                for (int r = 0; r < RT; ++r) mma16816(s[r][j], a[r], b0, b1);
+                            }
+                        }
+                    }
+                    const uint32_t sc = st + Stage::kK + Stage::kV;
+                    const float ks[2] = {lds32f(sc), lds32f(sc + 4)}, vs[2] = {lds32f(sc + 8), lds32f(sc + 12)};
+                    const float ev[2] = {__log2f(fmaxf(vs[0], 0x1p-126f)), __log2f(fmaxf(vs[1], 0x1p-126f))};
+
+                    // which keys the rows see
+                    bool clean = false;
+                    for (int x = 0; x < dnf.n_terms; ++x)
+                        clean = clean || (s_seq.clean_lo[x] <= tok && tok + kTileTokens - 1 <= s_seq.clean_hi[x]);
+                    uint32_t bits[RT][2];
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            bits[r][h] = 0xFFFFFFFFu;
+                            if (!clean) {
+                                bits[r][h] = 0;
+                                for (int x = 0; x < dnf.n_terms; ++x) {
+                                    int64_t lo, hi;
+                                    term_interval(dnf, x, pos[r][h], 0, len - 1, 0, 0, lo, hi);
+                                    bits[r][h] |= range_bits(lo, hi, tok);
+                                }
+                            }
+                        }
+
+                    uint32_t pa[RT][2][4];
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) {
+                        float top[2][2];  // [row][16-token half]
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            top[h][0] = top[h][1] = -INFINITY;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                                for (int y = 0; y < 2; ++y) {
+                                    float z = s[r][j][2 * h + y] * (qs[r][h] * ks[j >> 1]);
+                                    if (MODS) {
+                                        const float bias =
+                                            slope[r][h] * static_cast<float>(static_cast<int>(tok + 8 * j + 2 * t + y - pos[r][h]));
+                                        if (p.alibi_first) z += bias;
+                                        // cap * tanh(z / cap), tanh(u) = 1 - 2 / (exp(2 u) + 1)
+                                        if (p.softcap)
+                                            z = p.cap * (1.f - __fdividef(2.f, exp2_fast(z * (2.f * kLog2e / p.cap)) + 1.f));
+                                        if (!p.alibi_first) z += bias;
+                                        z *= kLog2e;
+                                    }
+                                    if (!(bits[r][h] >> (8 * j + 2 * t + y) & 1u)) z = -INFINITY;
+                                    s[r][j][2 * h + y] = z;
+                                    top[h][j >> 1] = fmaxf(top[h][j >> 1], z);
+                                }
+                        }
+                        float al[2], ao[2], cf[2][2], ref[2];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                top[h][x] = fmaxf(top[h][x], __shfl_xor_sync(0xFFFFFFFFu, top[h][x], 1));
+                                top[h][x] = fmaxf(top[h][x], __shfl_xor_sync(0xFFFFFFFFu, top[h][x], 2));
+                            }
+                            const float mn = fmaxf(m[r][h], fmaxf(top[h][0], top[h][1]));
+                            const float mon = fmaxf(mo[r][h], fmaxf(top[h][0] + ev[0], top[h][1] + ev[1]));
+                            ref[h] = mn == -INFINITY ? 0.f : mn;
+                            const float refo = mon == -INFINITY ? 0.f : mon;
+                            al[h] = exp2_fast(m[r][h] - ref[h]);
+                            ao[h] = exp2_fast(mo[r][h] - refo);
+                            const float shift = exp2_fast(ref[h] - refo);
+                            cf[h][0] = vs[0] * shift;
+                            cf[h][1] = vs[1] * shift;
+                            if (mn == -INFINITY) cf[h][0] = cf[h][1] = 0.f;
+                            m[r][h] = mn;
+                            mo[r][h] = mon;
+                        }
+                        if (__any_sync(0xFFFFFFFFu, ao[0] != 1.f || ao[1] != 1.f)) {
+#pragma unroll
+                            for (int x = 0; x < kOut; ++x) {
+                                o[r][x][0] *= ao[0];
+                                o[r][x][1] *= ao[0];
+                                o[r][x][2] *= ao[1];
+                                o[r][x][3] *= ao[1];
+                            }
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float sum = 0.f;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float a = exp2_fast(s[r][j][2 * h] - ref[h]), b = exp2_fast(s[r][j][2 * h + 1] - ref[h]);
+                                sum += a + b;
+                                // P to 11 bits: an error of 2^-12 of each term, below the output's bf16 rounding
+                                const __half2 v = __floats2half2_rn(a * cf[h][j >> 1], b * cf[h][j >> 1]);
+                                pa[r][j >> 1][h + 2 * (j & 1)] = *reinterpret_cast<const uint32_t*>(&v);
+                            }
+                            l[r][h] = l[r][h] * al[h] + sum;
+                        }
+                    }
+
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {  // 16 tokens
+                        uint32_t vw[4][D / 32];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const uint32_t a = st + Stage::kK + ((h * 4 + x) * 32 + lane) * (D / 8);
+                            if (D == 128) {
+                                const uint4 v = lds128(a);
+                                vw[x][0] = v.x, vw[x][1] = v.y, vw[x][D / 32 - 2] = v.z, vw[x][D / 32 - 1] = v.w;
+                            } else {
+                                const uint2 v = lds64(a);
+                                vw[x][0] = v.x, vw[x][1] = v.y;
+                            }
+                        }
+                        if (!INT8 && !clean) {
+                            // 0 * NaN: a NaN code that some row does not see must not reach that row. Rare
+                            // (NaN values in a tile on the mask's edge): the codes become 0 here, and rows
+                            // that see one get NaN from a product of visibility and NaN indicators.
+                            uint32_t found = 0;
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                                for (int y = 0; y < D / 32; ++y) found |= ((vw[x][y] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                            if (__any_sync(0xFFFFFFFFu, found != 0u)) {
+                                uint32_t see[RT][4];
+#pragma unroll
+                                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                                    for (int z = 0; z < 4; ++z) {
+                                        const uint32_t b = bits[r][z & 1] >> (16 * h + 8 * (z >> 1) + 2 * t);
+                                        see[r][z] = ((b & 1u) ? 0x3C00u : 0u) | ((b & 2u) ? 0x3C000000u : 0u);
+                                    }
+#pragma unroll
+                                for (int y = 0; y < D / 32; ++y) {
+                                    uint32_t ind[4];
+#pragma unroll
+                                    for (int x = 0; x < 4; ++x) {
+                                        const uint32_t nan =
+                                            ((((vw[x][y] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu;
+                                        vw[x][y] &= ~nan;
+                                        ind[x] = nan & 0x38383838u;  // e4m3 1.0
+                                    }
+                                    const uint32_t x0 = __byte_perm(ind[0], ind[1], 0x5140), x1 = __byte_perm(ind[0], ind[1], 0x7362);
+                                    const uint32_t y0 = __byte_perm(ind[2], ind[3], 0x5140), y1 = __byte_perm(ind[2], ind[3], 0x7362);
+#pragma unroll
+                                    for (int b = 0; b < 4; ++b) {
+                                        const uint32_t ux = b < 2 ? x0 : x1, uy = b < 2 ? y0 : y1;
+                                        const uint32_t b0 = (b & 1) ? halves_of<INT8, false>(ux) : halves_of<INT8, true>(ux);
+                                        const uint32_t b1 = (b & 1) ? halves_of<INT8, false>(uy) : halves_of<INT8, true>(uy);
+#pragma unroll
+                                        for (int r = 0; r < RT; ++r) {
+                                            float hit[4] = {0.f, 0.f, 0.f, 0.f};
+                                            mma16816(hit, see[r], b0, b1);
+#pragma unroll
+                                            for (int z = 0; z < 4; ++z)
+                                                if (hit[z] > 0.f) o[r][4 * y + b][z] = __int_as_float(0x7FFFFFFF);
+                                        }
+                                    }
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int y = 0; y < D / 32; ++y) {
+                            // 4 x 4 bytes: token-major words -> for each column its four tokens
+                            const uint32_t w0 = flip<INT8>(vw[0][y]), w1 = flip<INT8>(vw[1][y]), w2 = flip<INT8>(vw[2][y]),
+                                           w3 = flip<INT8>(vw[3][y]);
+                            const uint32_t x0 = __byte_perm(w0, w1, 0x5140), x1 = __byte_perm(w0, w1, 0x7362);
+                            const uint32_t y0 = __byte_perm(w2, w3, 0x5140), y1 = __byte_perm(w2, w3, 0x7362);
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) {
+                                const uint32_t ux = b < 2 ? x0 : x1, uy = b < 2 ? y0 : y1;
+                                const uint32_t b0 = (b & 1) ? halves_of<INT8, false>(ux) : halves_of<INT8, true>(ux);
+                                const uint32_t b1 = (b & 1) ? halves_of<INT8, false>(uy) : halves_of<INT8, true>(uy);
+#pragma unroll
+                                for (int r = 0; r < RT; ++r) mma16816(o[r][4 * y + b], pa[r][h], b0, b1);
+                            }
+                        }
+                    }
+                }
+                __syncwarp();  // every lane has read the stage's scales
+#pragma unroll
+                for (int x = 0; x + 1 < Stage::kStages; ++x) tok_q[x] = tok_q[x + 1];
+                tok_q[Stage::kStages - 1] = next_tok;
+                issue(stage);
+                stage = stage + 1 == Stage::kStages ? 0 : stage + 1;
+            }
+            cp_async_wait<0>();
+
+            // ---- the four warps' parts of the segment become one
+            __syncthreads();
+            constexpr int kPitch = D + 4;
+            float* s_o = reinterpret_cast<float*>(smem);                       // [warp][row][kPitch]
+            float* s_m = s_o + kPagedWarps * kRows * kPitch;                   // [warp][row][4]
+            static_assert(kPagedWarps * kRows * (kPitch + 4) * 4 <= Stage::kSmem, "the parts fit the stages");
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float sum = l[r][h];
+                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+                    const int row = warp * kRows + 16 * r + 8 * h + g;
+                    if (t == 0) {
+                        s_m[row * 4] = m[r][h];
+                        s_m[row * 4 + 1] = mo[r][h];
+                        s_m[row * 4 + 2] = sum;
+                    }
+                    // column c of output tile x holds d = c * (D / 8) + x
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int x = 0; x < kOut; x += 4)
+                            *reinterpret_cast<float4*>(s_o + row * kPitch + (2 * t + y) * (D / 8) + x) =
+                                make_float4(o[r][x][2 * h + y], o[r][x + 1][2 * h + y], o[r][x + 2][2 * h + y],
+                                            o[r][x + 3][2 * h + y]);
+                }
+            __syncthreads();
+            const bool whole = t0 == 0 && t1 == tiles;
+            const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (first_segment ? 0 : 1);
+            if (!whole && t0 == 0 && tid == 0) {
+                int32_t* hd = p.heads_of_parts + blockIdx.x * 8;
+                hd[1] = first_segment ? 0 : 1;
+                hd[2] = static_cast<int32_t>(s_seq.s.q0);
+                hd[3] = count;
+                hd[4] = head;
+                hd[5] = static_cast<int32_t>(row0 & 0xFFFFFFFF);
+                hd[6] = static_cast<int32_t>(row0 >> 32);
+                hd[0] = 1 + static_cast<int32_t>((tiles - t1 + share - 1) / share);
+            }
+            for (int x = tid; x < kRows * (D / 4); x += kPagedThreads) {
+                const int row = x / (D / 4), d = (x % (D / 4)) * 4;
+                if (row0 + row >= rows_all) continue;
+                float mm = -INFINITY, mmo = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kPagedWarps; ++w) {
+                    mm = fmaxf(mm, s_m[(w * kRows + row) * 4]);
+                    mmo = fmaxf(mmo, s_m[(w * kRows + row) * 4 + 1]);
+                }
+                const float ref = mm == -INFINITY ? 0.f : mm, refo = mmo == -INFINITY ? 0.f : mmo;
+                float sum = 0.f;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kPagedWarps; ++w) {
+                    const float* sm = s_m + (w * kRows + row) * 4;
+                    sum += sm[2] * exp2_fast(sm[0] - ref);
+                    const float f = exp2_fast(sm[1] - refo);
+                    const float4 v = *reinterpret_cast<const float4*>(s_o + (w * kRows + row) * kPitch + d);
+                    acc.x = fmaf(f, v.x, acc.x);
+                    acc.y = fmaf(f, v.y, acc.y);
+                    acc.z = fmaf(f, v.z, acc.z);
+                    acc.w = fmaf(f, v.w, acc.w);
+                }
+                if (whole) {
+                    const int64_t qi = (row0 + row) / p.group;
+                    const int hq = head * p.group + static_cast<int>(row0 + row - qi * p.group);
+                    // (a NaN sum is a row whose scores are NaN)
+                    const float f = sum == 0.f ? 0.f : exp2_fast(refo - ref) / sum;
+                    const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * f, acc.y * f), b = __floats2bfloat162_rn(acc.z * f, acc.w * f);
+                    *reinterpret_cast<uint2*>(p.out + ((s_seq.s.q0 + qi) * p.Hq + hq) * D + d) =
+                        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+                    if (d == 0)
+                        p.lse[static_cast<int64_t>(hq) * p.T + s_seq.s.q0 + qi] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+                } else {
+                    *reinterpret_cast<float4*>(p.part_o + (slot * kRows + row) * D + d) = acc;
+                    if (d == 0) *reinterpret_cast<float4*>(p.part_m + (slot * kRows + row) * 4) = make_float4(mm, mmo, sum, 0.f);
+                }
+            }
+            __syncthreads();
+            first_segment = false;
+            off += t1 - t0;
+            left -= t1 - t0;
+        }
+    }
+}
+
+// Joins the parts of the units that share boundaries cut: a unit that begins in
+// block b ends in block b + parts - 1, and its later parts are those blocks'
+// first. One block for each (block b, row); its warps take every fourth part.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kPagedThreads) paged_combine_kernel(const __grid_constant__ PagedParams p) {
+    constexpr float kLn2 = 0.6931471805599453f;
+    constexpr int kPer = D / 32;  // columns of one lane
+    __shared__ float s_o[kPagedWarps][D];
+    const int32_t* hd = p.heads_of_parts + blockIdx.x * 8;
+    const int parts = hd[0];
+    if (parts == 0) return;
+    const int64_t row0 = static_cast<int64_t>(static_cast<uint32_t>(hd[5])) | static_cast<int64_t>(hd[6]) << 32;
+    const int64_t row = row0 + blockIdx.y;
+    if (row >= static_cast<int64_t>(hd[3]) * p.group) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto slot_of = [&](int j) -> int64_t {
+        return (2 * (static_cast<int64_t>(blockIdx.x) + j) + (j == 0 ? hd[1] : 0)) * ROWS + blockIdx.y;
+    };
+    float m = -INFINITY, mo = -INFINITY;
+    for (int j = lane; j < parts; j += 32) {
+        const float4 v = *reinterpret_cast<const float4*>(p.part_m + slot_of(j) * 4);
+        m = fmaxf(m, v.x);
+        mo = fmaxf(mo, v.y);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+        mo = fmaxf(mo, __shfl_xor_sync(0xFFFFFFFFu, mo, d));
+    }
+    const float ref = m == -INFINITY ? 0.f : m, refo = mo == -INFINITY ? 0.f : mo;
+    float sum = 0.f;
+    for (int j = lane; j < parts; j += 32) {
+        const float4 v = *reinterpret_cast<const float4*>(p.part_m + slot_of(j) * 4);
+        sum += v.z * exp2_fast(v.x - ref);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    float acc[kPer];
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
+#pragma unroll 4
+    for (int j = warp; j < parts; j += kPagedWarps) {
+        const int64_t s = slot_of(j);
+        const float f = exp2_fast(p.part_m[s * 4 + 1] - refo);
+        const float* src = p.part_o + s * D + lane * kPer;
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) acc[x] = fmaf(f, src[x], acc[x]);
+    }
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) s_o[warp][lane * kPer + x] = acc[x];
+    __syncthreads();
+    const int64_t qi = row / p.group;
+    const int hq = hd[4] * p.group + static_cast<int>(row - qi * p.group);
+    const int64_t token = hd[2] + qi;
+    const float f = sum == 0.f ? 0.f : exp2_fast(refo - ref) / sum;
+    for (int d = threadIdx.x; d < D; d += kPagedThreads) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kPagedWarps; ++w) v += s_o[w][d];
+        p.out[(token * p.Hq + hq) * D + d] = __float2bfloat16_rn(v * f);
+    }
+    if (threadIdx.x == 0) p.lse[static_cast<int64_t>(hq) * p.T + token] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+}
+
+}  // namespace bsmt

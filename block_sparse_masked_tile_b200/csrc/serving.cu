@@ -1,0 +1,515 @@
+// libbsmt: rotary positions, the 8-bit paged cache, and attention over it (the
+// entry points of include/bsmt_serving.h, that a server calls beside flex_attention).
+//
+// Host side: argument checks and launches. Nothing here allocates device memory
+// and nothing synchronizes.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <mutex>
+
+#include "bsmt_serving.h"
+#include "host_common.h"
+#include "kv_cache.cuh"
+#include "paged_attn.cuh"
+#include "rotary.cuh"
+
+using namespace bsmt_host;
+
+namespace {
+
+constexpr int kMaxSeqs = 1 << 18;  // one bit each in the page planners' shared memory
+constexpr int kMaxPartBlocks = 1024;
+
+bsmt_status launched(const char* what) {
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(BSMT_ERR_CUDA, "%s launch: %s", what, cudaGetErrorString(e));
+    return BSMT_OK;
+}
+
+bsmt_status device(int* dev, int* nsm, int** status) {
+    const bsmt_status st = sm_count(dev, nsm);
+    return st != BSMT_OK ? st : status_word(*dev, status);
+}
+
+// Checks the cache and gives the kernels' form of it.
+bsmt_status check_cache(const bsmt_kv_cache* in, bsmt::KvCache* out) {
+    if (in == nullptr) return fail(BSMT_ERR_INVALID_ARGUMENT, "cache is NULL");
+    if (in->head_dim != 64 && in->head_dim != 128)
+        return fail(BSMT_ERR_UNSUPPORTED, "cache head_dim=%d (supported: 64, 128)", in->head_dim);
+    if (in->page_size != 16 && in->page_size != 32 && in->page_size != 64 && in->page_size != 128)
+        return fail(BSMT_ERR_UNSUPPORTED, "cache page_size=%d (supported: 16, 32, 64, 128)", in->page_size);
+    if (in->dtype != BSMT_CACHE_E4M3 && in->dtype != BSMT_CACHE_INT8)
+        return fail(BSMT_ERR_UNSUPPORTED, "cache dtype %d", in->dtype);
+    if (in->num_layers < 1 || in->num_pages < 1 || in->num_kv_heads < 1 || in->max_seqs < 1 || in->max_pages < 1)
+        return fail(BSMT_ERR_INVALID_ARGUMENT, "cache sizes must be positive (layers %d, pages %d, kv heads %d, seqs %d, pages a seq %d)",
+                    in->num_layers, in->num_pages, in->num_kv_heads, in->max_seqs, in->max_pages);
+    if (in->max_seqs > kMaxSeqs) return fail(BSMT_ERR_UNSUPPORTED, "cache max_seqs=%d above %d", in->max_seqs, kMaxSeqs);
+    if (in->num_kv_heads > 65535) return fail(BSMT_ERR_UNSUPPORTED, "cache num_kv_heads=%d above 65535", in->num_kv_heads);
+    if (in->num_pages > (1 << 30)) return fail(BSMT_ERR_UNSUPPORTED, "cache num_pages=%d above 2^30", in->num_pages);
+    if (int64_t(in->max_pages) * in->page_size > kMaxLen)
+        return fail(BSMT_ERR_UNSUPPORTED, "cache: %d pages of %d tokens a sequence, above %lld tokens", in->max_pages,
+                    in->page_size, static_cast<long long>(kMaxLen));
+    if (!in->k || !in->v || !in->k_scale || !in->v_scale || !in->page_table || !in->seq_lens || !in->ref_counts)
+        return fail(BSMT_ERR_INVALID_ARGUMENT, "cache pointers must be non-NULL");
+    if (!aligned(in->k, 16) || !aligned(in->v, 16) || !aligned(in->ref_counts, 16))
+        return fail(BSMT_ERR_INVALID_ARGUMENT, "cache k, v and ref_counts must be 16-byte aligned");
+    if (!aligned(in->k_scale, 4) || !aligned(in->v_scale, 4) || !aligned(in->page_table, 4) || !aligned(in->seq_lens, 4))
+        return fail(BSMT_ERR_INVALID_ARGUMENT, "cache scales, page_table and seq_lens must be 4-byte aligned");
+    out->k = static_cast<uint8_t*>(in->k);
+    out->v = static_cast<uint8_t*>(in->v);
+    out->k_scale = in->k_scale;
+    out->v_scale = in->v_scale;
+    out->page_table = in->page_table;
+    out->seq_lens = in->seq_lens;
+    out->ref_counts = in->ref_counts;
+    out->layers = in->num_layers;
+    out->pages = in->num_pages;
+    out->heads = in->num_kv_heads;
+    out->page = in->page_size;
+    out->page_shift = in->page_size == 16 ? 4 : in->page_size == 32 ? 5 : in->page_size == 64 ? 6 : 7;
+    out->dim = in->head_dim;
+    out->max_seqs = in->max_seqs;
+    out->max_pages = in->max_pages;
+    out->int8 = in->dtype == BSMT_CACHE_INT8;
+    return BSMT_OK;
+}
+
+bsmt_status check_layer(const bsmt::KvCache& c, int32_t layer) {
+    if (layer < 0 || layer >= c.layers) return fail(BSMT_ERR_INVALID_ARGUMENT, "layer %d outside [0, %d)", layer, c.layers);
+    return BSMT_OK;
+}
+
+// A list of n int32 on the device.
+bsmt_status check_list(const char* name, const int32_t* p, int64_t n, bool optional = false) {
+    if (p == nullptr && !optional && n > 0) return fail(BSMT_ERR_INVALID_ARGUMENT, "%s is NULL", name);
+    if (!aligned(p, 4)) return fail(BSMT_ERR_INVALID_ARGUMENT, "%s must be 4-byte aligned", name);
+    return BSMT_OK;
+}
+
+bsmt_status check_count(int64_t n, int64_t T, const int32_t* cu) {
+    if (n < 0 || T < 0) return fail(BSMT_ERR_INVALID_ARGUMENT, "negative size (%lld sequences, %lld tokens)",
+                                    static_cast<long long>(n), static_cast<long long>(T));
+    if (n > (1 << 24) || T > kMaxLen) return fail(BSMT_ERR_UNSUPPORTED, "%lld sequences, %lld tokens", static_cast<long long>(n),
+                                                  static_cast<long long>(T));
+    if (cu == nullptr && n != T)
+        return fail(BSMT_ERR_SHAPE_MISMATCH, "%lld tokens for %lld sequences: cu_seqlens is needed unless there is one each",
+                    static_cast<long long>(T), static_cast<long long>(n));
+    return BSMT_OK;
+}
+
+bsmt_status check_workspace(const void* ws, int64_t have, int64_t need) {
+    if (ws == nullptr || !aligned(ws, 256))
+        return fail(BSMT_ERR_INVALID_ARGUMENT, "workspace must be non-NULL and 256-byte aligned");
+    if (have < need)
+        return fail(BSMT_ERR_INVALID_ARGUMENT, "workspace holds %lld bytes, %lld needed", static_cast<long long>(have),
+                    static_cast<long long>(need));
+    return BSMT_OK;
+}
+
+int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+#define TRY(x)                             \
+    do {                                   \
+        const bsmt_status st_ = (x);       \
+        if (st_ != BSMT_OK) return st_;    \
+    } while (0)
+
+// ------------------------------------------------------------------ rotary
+namespace {
+template <typename E>
+void launch_rotary(const bsmt::RotaryParams& p, int vec, bool interleaved, dim3 grid, cudaStream_t s) {
+    constexpr int n = bsmt::kRotaryThreads;
+    if (vec == 8) {
+        if (interleaved)
+            bsmt::rotary_kernel<E, 8, true><<<grid, n, 0, s>>>(p);
+        else
+            bsmt::rotary_kernel<E, 8, false><<<grid, n, 0, s>>>(p);
+    } else {
+        if (interleaved)
+            bsmt::rotary_kernel<E, 1, true><<<grid, n, 0, s>>>(p);
+        else
+            bsmt::rotary_kernel<E, 1, false><<<grid, n, 0, s>>>(p);
+    }
+}
+}  // namespace
+
+extern "C" bsmt_status bsmt_rotary(const bsmt_rotary_spec* spec, int32_t dtype, int64_t B, int64_t T,
+                                   const int32_t* positions, const int64_t position_strides[3], int32_t inverse,
+                                   const bsmt_rotary_tensor* tensors, int32_t num_tensors, void* stream) {
+    if (spec == nullptr || tensors == nullptr || position_strides == nullptr)
+        return fail(BSMT_ERR_INVALID_ARGUMENT, "rotary: spec, tensors and position_strides must be non-NULL");
+    if (dtype != BSMT_BF16 && dtype != BSMT_FP32) return fail(BSMT_ERR_UNSUPPORTED, "rotary dtype %d", dtype);
+    if (num_tensors < 1 || num_tensors > 2) return fail(BSMT_ERR_INVALID_ARGUMENT, "rotary: %d tensors (1 or 2)", num_tensors);
+    if (B < 0 || T < 0) return fail(BSMT_ERR_INVALID_ARGUMENT, "negative size (B=%lld T=%lld)", static_cast<long long>(B), static_cast<long long>(T));
+    if (T > kMaxLen || (T > 0 && B > (int64_t(1) << 40) / T)) return fail(BSMT_ERR_UNSUPPORTED, "rotary: B=%lld T=%lld", static_cast<long long>(B), static_cast<long long>(T));
+    if (spec->num_pairs < 1 || spec->num_pairs > BSMT_MAX_ROTARY_PAIRS || spec->head_dim < 2 * spec->num_pairs)
+        return fail(BSMT_ERR_INVALID_ARGUMENT, "rotary: %d pairs in a head of %d (1 to %d pairs)", spec->num_pairs, spec->head_dim,
+                    BSMT_MAX_ROTARY_PAIRS);
+    if (spec->num_axes < 1 || spec->num_axes > 127) return fail(BSMT_ERR_INVALID_ARGUMENT, "rotary: %d axes", spec->num_axes);
+    bsmt::RotaryParams p;
+    std::memset(&p, 0, sizeof(p));
+    for (int i = 0; i < spec->num_pairs; ++i) {
+        const double f = spec->inv_freq[i];
+        if (!std::isfinite(f)) return fail(BSMT_ERR_INVALID_ARGUMENT, "rotary: inv_freq[%d] is not finite", i);
+        if (spec->axis[i] < 0 || spec->axis[i] >= spec->num_axes)
+            return fail(BSMT_ERR_INVALID_ARGUMENT, "rotary: pair %d has axis %d of %d", i, spec->axis[i], spec->num_axes);
+        // the fraction of a turn, in 2^-64 turns (whole turns drop out)
+        const long double turns = static_cast<long double>(f) / 6.283185307179586476925286766559L;
+        const long double part = turns - std::floor(turns);
+        p.turn[i] = part < 1.0L ? static_cast<uint64_t>(part * 18446744073709551616.0L) : 0;
+        p.axis[i] = spec->axis[i];
+    }
+    int64_t heads = 0;
+    const int64_t size = dtype == BSMT_BF16 ? 2 : 4;
+    bool wide = spec->num_pairs % 8 == 0;
+    for (int i = 0; i < num_tensors; ++i) {
+        const bsmt_rotary_tensor& x = tensors[i];
+        if (x.heads < 0) return fail(BSMT_ERR_INVALID_ARGUMENT, "rotary: tensor %d has %d heads", i, x.heads);
+        if (B * T > 0 && x.heads > 0 && (!x.in || !x.out)) return fail(BSMT_ERR_INVALID_ARGUMENT, "rotary: tensor %d is NULL", i);
+        if (!aligned(x.in, size) || !aligned(x.out, size)) return fail(BSMT_ERR_INVALID_ARGUMENT, "rotary: tensor %d is misaligned", i);
+        wide = wide && aligned(x.in, 16) && aligned(x.out, 16);
+        for (int j = 0; j < 3; ++j) wide = wide && x.in_strides[j] * size % 16 == 0 && x.out_strides[j] * size % 16 == 0;
+        p.x[i] = {x.in, x.out, x.in_strides[0], x.in_strides[1], x.in_strides[2], x.out_strides[0], x.out_strides[1], x.out_strides[2], x.heads};
+        heads += x.heads;
+    }
+    if (heads > 65535) return fail(BSMT_ERR_UNSUPPORTED, "rotary: %lld heads", static_cast<long long>(heads));
+    if (B * T == 0 || heads == 0) return ok();
+    TRY(check_list("positions", positions, 1));
+    int dev = 0, nsm = 0;
+    TRY(sm_count(&dev, &nsm));
+    p.pos = positions;
+    p.pos_axis = position_strides[0];
+    p.pos_b = position_strides[1];
+    p.pos_t = position_strides[2];
+    p.tokens = B * T;
+    p.T = static_cast<int32_t>(T);
+    p.head_dim = spec->head_dim;
+    p.pairs = spec->num_pairs;
+    p.heads = static_cast<int32_t>(heads);
+    p.inverse = inverse != 0;
+    const int vec = wide ? 8 : 1;
+    const int64_t units = p.tokens * (spec->num_pairs / vec);
+    const int64_t blocks = (units + bsmt::kRotaryThreads - 1) / bsmt::kRotaryThreads;
+    if (blocks > 0x7FFFFFFF) return fail(BSMT_ERR_UNSUPPORTED, "rotary: grid too large");
+    // A thread's sines serve `chunk` heads: as many as leave some 16 blocks an SM.
+    int64_t cuts = std::max<int64_t>(1, std::min<int64_t>(heads, 16 * int64_t(nsm) / blocks));
+    p.chunk = static_cast<int32_t>((heads + cuts - 1) / cuts);
+    cuts = (heads + p.chunk - 1) / p.chunk;
+    const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(cuts));
+    if (dtype == BSMT_BF16)
+        launch_rotary<__nv_bfloat16>(p, vec, spec->interleaved != 0, grid, static_cast<cudaStream_t>(stream));
+    else
+        launch_rotary<float>(p, vec, spec->interleaved != 0, grid, static_cast<cudaStream_t>(stream));
+    TRY(launched("rotary"));
+    return ok();
+}
+
+// ------------------------------------------------------------------- cache
+extern "C" bsmt_status bsmt_cache_write(const bsmt_kv_cache* cache, int32_t layer, const int32_t* seqs, const int32_t* starts,
+                                        int64_t n, const int32_t* cu_seqlens, const void* k, const void* v, int64_t T,
+                                        const int64_t k_strides[2], const int64_t v_strides[2], void* stream) {
+    bsmt::CacheWriteParams p;
+    TRY(check_cache(cache, &p.c));
+    TRY(check_layer(p.c, layer));
+    TRY(check_count(n, T, cu_seqlens));
+    TRY(check_list("seqs", seqs, n));
+    TRY(check_list("starts", starts, n));
+    TRY(check_list("cu_seqlens", cu_seqlens, 1, true));
+    if (n == 0 || T == 0) return ok();
+    if (!k || !v || !k_strides || !v_strides) return fail(BSMT_ERR_INVALID_ARGUMENT, "k, v and their strides must be non-NULL");
+    for (int i = 0; i < 2; ++i)
+        if (k_strides[i] % 8 != 0 || v_strides[i] % 8 != 0 || k_strides[i] < 0 || v_strides[i] < 0)
+            return fail(BSMT_ERR_INVALID_ARGUMENT, "k and v strides must be multiples of 8 elements");
+    if (!aligned(k, 16) || !aligned(v, 16)) return fail(BSMT_ERR_INVALID_ARGUMENT, "k and v must be 16-byte aligned");
+    int dev = 0, nsm = 0;
+    TRY(device(&dev, &nsm, &p.status));
+    p.seqs = seqs;
+    p.starts = starts;
+    p.cu = cu_seqlens;
+    p.k = static_cast<const __nv_bfloat16*>(k);
+    p.v = static_cast<const __nv_bfloat16*>(v);
+    p.kt = k_strides[0];
+    p.kh = k_strides[1];
+    p.vt = v_strides[0];
+    p.vh = v_strides[1];
+    p.T = T;
+    p.n = static_cast<int32_t>(n);
+    p.layer = layer;
+    p.items = cu_seqlens == nullptr ? n : (T >> p.c.page_shift) + 2 * n;
+    // A warp for calls of at most four tokens a sequence on average, a block of 256 otherwise.
+    const bool small = T <= 4 * n;
+    const int64_t units = p.items * 2 * p.c.heads;
+    const int64_t blocks = small ? (units + 7) / 8 : units;
+    if (blocks > 0x7FFFFFFF) return fail(BSMT_ERR_UNSUPPORTED, "cache_write: grid too large");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const unsigned grid = static_cast<unsigned>(blocks);
+    if (p.c.int8) {
+        if (small)
+            bsmt::cache_write_kernel<32, true><<<grid, 256, 0, s>>>(p);
+        else
+            bsmt::cache_write_kernel<256, true><<<grid, 256, 0, s>>>(p);
+    } else {
+        if (small)
+            bsmt::cache_write_kernel<32, false><<<grid, 256, 0, s>>>(p);
+        else
+            bsmt::cache_write_kernel<256, false><<<grid, 256, 0, s>>>(p);
+    }
+    TRY(launched("cache_write"));
+    return ok();
+}
+
+extern "C" bsmt_status bsmt_cache_gather(const bsmt_kv_cache* cache, int32_t layer, const int32_t* seqs, const int32_t* starts,
+                                         int64_t n, const int32_t* cu_seqlens, int64_t T, void* k, void* v, void* stream) {
+    bsmt::CacheGatherParams p;
+    TRY(check_cache(cache, &p.c));
+    TRY(check_layer(p.c, layer));
+    TRY(check_count(n, T, cu_seqlens));
+    TRY(check_list("seqs", seqs, n));
+    TRY(check_list("starts", starts, n, true));
+    TRY(check_list("cu_seqlens", cu_seqlens, 1, true));
+    if (T == 0) return ok();
+    if (!k || !v || !aligned(k, 16) || !aligned(v, 16))
+        return fail(BSMT_ERR_INVALID_ARGUMENT, "k and v must be non-NULL and 16-byte aligned");
+    int dev = 0, nsm = 0;
+    TRY(device(&dev, &nsm, &p.status));
+    p.seqs = seqs;
+    p.starts = starts;
+    p.cu = cu_seqlens;
+    p.k = static_cast<__nv_bfloat16*>(k);
+    p.v = static_cast<__nv_bfloat16*>(v);
+    p.T = T;
+    p.n = static_cast<int32_t>(n);
+    p.layer = layer;
+    const unsigned grid = static_cast<unsigned>((T + bsmt::kGatherTokens - 1) / bsmt::kGatherTokens);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (p.c.int8)
+        bsmt::cache_gather_kernel<true><<<grid, 256, 0, s>>>(p);
+    else
+        bsmt::cache_gather_kernel<false><<<grid, 256, 0, s>>>(p);
+    TRY(launched("cache_gather"));
+    return ok();
+}
+
+// ------------------------------------------------------------------- pages
+extern "C" bsmt_status bsmt_cache_workspace_bytes(const bsmt_kv_cache* cache, int64_t n, int64_t* bytes) {
+    if (cache == nullptr || bytes == nullptr) return fail(BSMT_ERR_INVALID_ARGUMENT, "cache and bytes must be non-NULL");
+    if (cache->num_pages < 1 || n < 0 || n > (1 << 24))
+        return fail(BSMT_ERR_INVALID_ARGUMENT, "%d pages, %lld sequences", cache->num_pages, static_cast<long long>(n));
+    *bytes = 256 + std::max<int64_t>(3 * round256(int64_t(cache->num_pages) * 4), round256(int64_t(cache->num_pages) * 4) + round256(n * 8));
+    return ok();
+}
+
+extern "C" bsmt_status bsmt_cache_extend(const bsmt_kv_cache* cache, const int32_t* seqs, const int32_t* counts, int64_t n,
+                                         int32_t* starts, void* workspace, int64_t workspace_bytes, void* stream) {
+    bsmt::CacheExtendParams p;
+    TRY(check_cache(cache, &p.c));
+    TRY(check_count(n, n, nullptr));
+    TRY(check_list("seqs", seqs, n));
+    TRY(check_list("counts", counts, n, true));
+    TRY(check_list("starts", starts, n));
+    if (n == 0) return ok();
+    int64_t need = 0;
+    TRY(bsmt_cache_workspace_bytes(cache, n, &need));
+    TRY(check_workspace(workspace, workspace_bytes, need));
+    int dev = 0, nsm = 0;
+    TRY(device(&dev, &nsm, &p.status));
+    p.seqs = seqs;
+    p.counts = counts;
+    p.starts = starts;
+    p.list = static_cast<int32_t*>(workspace);
+    p.n = static_cast<int32_t>(n);
+    const int bitmap = (p.c.max_seqs + 31) / 32 * 4;
+    bsmt::cache_extend_kernel<<<1, bsmt::kPlanThreads, bitmap, static_cast<cudaStream_t>(stream)>>>(p);
+    TRY(launched("cache_extend"));
+    return ok();
+}
+
+extern "C" bsmt_status bsmt_cache_fork(const bsmt_kv_cache* cache, const int32_t* src, const int32_t* dst, int64_t n,
+                                       void* workspace, int64_t workspace_bytes, void* stream) {
+    bsmt::CacheForkParams p;
+    TRY(check_cache(cache, &p.c));
+    TRY(check_count(n, n, nullptr));
+    TRY(check_list("src", src, n));
+    TRY(check_list("dst", dst, n));
+    if (n == 0) return ok();
+    int64_t need = 0;
+    TRY(bsmt_cache_workspace_bytes(cache, n, &need));
+    TRY(check_workspace(workspace, workspace_bytes, need));
+    int dev = 0, nsm = 0;
+    TRY(device(&dev, &nsm, &p.status));
+    p.src = src;
+    p.dst = dst;
+    p.list = static_cast<int32_t*>(workspace);
+    p.jobs = reinterpret_cast<int2*>(static_cast<char*>(workspace) + round256(int64_t(p.c.pages) * 4));
+    p.n = static_cast<int32_t>(n);
+    // Blocks of one fork: 32 KB of a whole page's codes each, and some 8 blocks an SM in all.
+    const int64_t most = int64_t(p.c.layers) * 2 * p.c.heads * p.c.page * p.c.dim;
+    p.blocks = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>((most + 32767) / 32768, std::max<int64_t>(2, 8 * int64_t(nsm) / n))));
+    const int bitmap = (p.c.max_seqs + 31) / 32 * 4;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    bsmt::cache_fork_plan_kernel<<<1, bsmt::kPlanThreads, bitmap, s>>>(p);
+    TRY(launched("cache_fork plan"));
+    bsmt::cache_fork_kernel<<<static_cast<unsigned>(n * p.blocks), 256, 0, s>>>(p);
+    TRY(launched("cache_fork"));
+    return ok();
+}
+
+extern "C" bsmt_status bsmt_cache_free(const bsmt_kv_cache* cache, const int32_t* seqs, int64_t n, void* stream) {
+    bsmt::KvCache c;
+    TRY(check_cache(cache, &c));
+    TRY(check_count(n, n, nullptr));
+    TRY(check_list("seqs", seqs, n));
+    if (n == 0) return ok();
+    int dev = 0, nsm = 0;
+    int* status = nullptr;
+    TRY(device(&dev, &nsm, &status));
+    bsmt::cache_free_kernel<<<static_cast<unsigned>(n), 256, 0, static_cast<cudaStream_t>(stream)>>>(c, seqs, status);
+    TRY(launched("cache_free"));
+    return ok();
+}
+
+extern "C" bsmt_status bsmt_cache_compact(const bsmt_kv_cache* cache, int32_t* live, void* workspace, int64_t workspace_bytes,
+                                          void* stream) {
+    bsmt::CacheCompactParams p;
+    TRY(check_cache(cache, &p.c));
+    TRY(check_list("live", live, 1));
+    int64_t need = 0;
+    TRY(bsmt_cache_workspace_bytes(cache, 0, &need));
+    TRY(check_workspace(workspace, workspace_bytes, need));
+    int dev = 0, nsm = 0;
+    TRY(device(&dev, &nsm, &p.status));
+    const int64_t list = round256(int64_t(p.c.pages) * 4) / 4;
+    p.live = live;
+    p.header = static_cast<int32_t*>(workspace);
+    p.holes = p.header + 64;
+    p.movers = p.holes + list;
+    p.to = p.movers + list;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    bsmt::cache_compact_plan_kernel<<<1, bsmt::kPlanThreads, 0, s>>>(p);
+    TRY(launched("cache_compact plan"));
+    bsmt::cache_compact_kernel<<<4 * nsm, 256, 0, s>>>(p);
+    TRY(launched("cache_compact"));
+    return ok();
+}
+
+// --------------------------------------------------------------- attention
+namespace {
+
+std::mutex g_paged_mu;
+bool g_paged_set[64][16] = {{false}};
+
+// O, the maxima and sums of two parts for each block, and the blocks' heads.
+int64_t paged_ws_bytes(int64_t D) {
+    return int64_t(kMaxPartBlocks) * 2 * 32 * (D + 4) * 4 + round256(int64_t(kMaxPartBlocks) * 32);
+}
+
+template <int D, bool INT8, int RT, bool MODS>
+bsmt_status launch_paged(int dev, int nsm, bsmt::PagedParams p, const bsmt::MaskDnf& dnf, cudaStream_t s) {
+    auto kern = bsmt::paged_attention_kernel<D, INT8, RT, MODS>;
+    constexpr int smem = bsmt::paged_smem<D, RT>();
+    {
+        std::lock_guard<std::mutex> lk(g_paged_mu);
+        bool& set = g_paged_set[dev][(D == 128 ? 8 : 0) + (INT8 ? 4 : 0) + (RT > 1 ? 2 : 0) + (MODS ? 1 : 0)];
+        if (!set) {
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return fail(BSMT_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+            set = true;
+        }
+    }
+    const int blocks = std::min(2 * nsm, kMaxPartBlocks);
+    kern<<<blocks, bsmt::kPagedThreads, smem, s>>>(p, dnf);
+    TRY(launched("paged_attention"));
+    bsmt::paged_combine_kernel<D, 16 * RT><<<dim3(blocks, 16 * RT), bsmt::kPagedThreads, 0, s>>>(p);
+    TRY(launched("paged_attention combine"));
+    return BSMT_OK;
+}
+
+template <int D, bool INT8>
+bsmt_status launch_paged_kind(int rt, bool mods, int dev, int nsm, const bsmt::PagedParams& p, const bsmt::MaskDnf& dnf, cudaStream_t s) {
+    if (rt == 1)
+        return mods ? launch_paged<D, INT8, 1, true>(dev, nsm, p, dnf, s) : launch_paged<D, INT8, 1, false>(dev, nsm, p, dnf, s);
+    return mods ? launch_paged<D, INT8, 2, true>(dev, nsm, p, dnf, s) : launch_paged<D, INT8, 2, false>(dev, nsm, p, dnf, s);
+}
+
+}  // namespace
+
+extern "C" bsmt_status bsmt_paged_attention_workspace_bytes(int64_t D, int64_t* bytes) {
+    if (bytes == nullptr) return fail(BSMT_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    if (D != 64 && D != 128) return fail(BSMT_ERR_UNSUPPORTED, "head dim D=%lld (supported: 64, 128)", static_cast<long long>(D));
+    *bytes = paged_ws_bytes(D);
+    return ok();
+}
+
+extern "C" bsmt_status bsmt_paged_attention(const void* q, int64_t T, int64_t Hq, const bsmt_kv_cache* cache, int32_t layer,
+                                            const int32_t* seqs, int64_t n, const int32_t* cu_seqlens_q,
+                                            const bsmt_mask_spec* mask_spec, const bsmt_score_spec* score, float scale,
+                                            int32_t enable_gqa, void* out, float* lse, void* workspace,
+                                            int64_t workspace_bytes, void* stream) {
+    bsmt::PagedParams p;
+    std::memset(&p, 0, sizeof(p));
+    TRY(check_cache(cache, &p.c));
+    TRY(check_layer(p.c, layer));
+    TRY(check_count(n, T, cu_seqlens_q));
+    TRY(check_list("seqs", seqs, n));
+    TRY(check_list("cu_seqlens_q", cu_seqlens_q, 1, true));
+    if (Hq < 1 || Hq > 65535 || Hq % p.c.heads != 0)
+        return fail(BSMT_ERR_SHAPE_MISMATCH, "Hq=%lld is not a multiple of the cache's %d kv heads", static_cast<long long>(Hq), p.c.heads);
+    if (Hq != p.c.heads && !enable_gqa)
+        return fail(BSMT_ERR_SHAPE_MISMATCH, "Hq=%lld != Hkv=%d requires enable_gqa", static_cast<long long>(Hq), p.c.heads);
+    if (T > 0 && (!q || !out || !lse)) return fail(BSMT_ERR_INVALID_ARGUMENT, "q, out and lse must be non-NULL");
+    if (!aligned(q, 16) || !aligned(out, 16)) return fail(BSMT_ERR_INVALID_ARGUMENT, "q and out must be 16-byte aligned");
+    if (!aligned(lse, 4)) return fail(BSMT_ERR_INVALID_ARGUMENT, "lse must be 4-byte aligned");
+    if (std::isnan(scale) || std::isinf(scale)) return fail(BSMT_ERR_INVALID_ARGUMENT, "scale must be finite");
+    if (scale <= 0.f) scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(p.c.dim)));
+    if (mask_spec != nullptr)
+        for (int i = 0; i < mask_spec->num_nodes && i < BSMT_MAX_MASK_NODES; ++i)
+            if (mask_spec->nodes[i].kind == BSMT_MASK_DOCUMENT)
+                return fail(BSMT_ERR_UNSUPPORTED, "paged attention: a cache's sequence is one document; DOCUMENT masks are not taken");
+    bsmt::MaskDnf dnf;
+    TRY(build_dnf(mask_spec, 1, &dnf));
+    ScoreArgs sa;
+    TRY(score_args(score, Hq, &sa));
+    if (T == 0) return ok();
+    TRY(check_workspace(workspace, workspace_bytes, paged_ws_bytes(p.c.dim)));
+    int dev = 0, nsm = 0;
+    TRY(device(&dev, &nsm, &p.status));
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.seqs = seqs;
+    p.cu = cu_seqlens_q;
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.lse = lse;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_m = p.part_o + int64_t(kMaxPartBlocks) * 2 * 32 * p.c.dim;
+    p.heads_of_parts = reinterpret_cast<int32_t*>(p.part_m + int64_t(kMaxPartBlocks) * 2 * 32 * 4);
+    p.slopes = sa.slopes;
+    p.T = T;
+    p.n = static_cast<int32_t>(n);
+    p.layer = layer;
+    p.Hq = static_cast<int32_t>(Hq);
+    p.group = static_cast<int32_t>(Hq / p.c.heads);
+    p.min_share = 8;  // two tiles for each warp of a block
+    p.scale = scale;
+    p.cap = sa.cap;
+    // the modes of the score program: none, soft-cap, ALiBi, soft-cap then ALiBi, ALiBi then soft-cap
+    p.softcap = sa.mode == 1 || sa.mode == 3 || sa.mode == 4;
+    p.alibi = sa.mode == 2 || sa.mode == 3 || sa.mode == 4;
+    p.alibi_first = sa.mode == 4;
+    p.alibi_h0 = sa.alibi_h0;
+    p.alibi_heads = sa.alibi_heads;
+    // Row tiles of 16, or two of them a block once an average sequence has more rows.
+    const int rt = T * p.group > 16 * std::max<int64_t>(n, 1) ? 2 : 1;
+    const bool mods = sa.mode != 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    bsmt_status st;
+    if (p.c.dim == 128)
+        st = p.c.int8 ? launch_paged_kind<128, true>(rt, mods, dev, nsm, p, dnf, s) : launch_paged_kind<128, false>(rt, mods, dev, nsm, p, dnf, s);
+    else
+        st = p.c.int8 ? launch_paged_kind<64, true>(rt, mods, dev, nsm, p, dnf, s) : launch_paged_kind<64, false>(rt, mods, dev, nsm, p, dnf, s);
+    if (st != BSMT_OK) return st;
+    return ok();
+}

@@ -1,6 +1,7 @@
 /*
  * bsmt.h: C ABI of libbsmt, block-sparse masked-tile attention (forward and
- * backward) for NVIDIA B200 (sm_100a).
+ * backward) for NVIDIA B200 (sm_100a). bsmt_serving.h holds the rest of it:
+ * rotary positions, a paged cache in 8 bits and attention over that.
  *
  * The library builds a block-sparse BlockMask from a composable mask
  * description. It then runs scaled-dot-product attention. The attention
@@ -60,8 +61,12 @@ typedef enum bsmt_status {
     BSMT_ERR_UNSUPPORTED = 3,        /* valid request outside what this build implements */
     BSMT_ERR_CUDA = 4,               /* a CUDA runtime or driver call failed */
     BSMT_ERR_DEVICE_TIMEOUT = 5,     /* device: a pipeline wait gave up (kernel returned early) */
-    BSMT_ERR_DEVICE_BOUNDS = 6,      /* device: a block index outside [0, KB) or lists not ascending */
-    BSMT_ERR_DEVICE_PRECONDITION = 7 /* device: kv document ids not non-decreasing */
+    BSMT_ERR_DEVICE_BOUNDS = 6,      /* device: a block index outside [0, KB) or lists not ascending; or
+                                        a cache's sequence, position or page out of range */
+    BSMT_ERR_DEVICE_PRECONDITION = 7,/* device: kv document ids not non-decreasing; or lists or pages
+                                        that do not meet a cache call's conditions */
+    BSMT_ERR_DEVICE_CAPACITY = 8     /* device: too few free pages in a cache, or too few places in a row
+                                        of its page table */
 } bsmt_status;
 
 /* ------------------------------------------------------------------ masks
