@@ -3,7 +3,7 @@
 //   out = softmax_j(mod(scale * q . k_j), masked) v,  k_j = code * k_scale[page, head]
 //
 // A unit is (sequence, row tile, kv head): a row is one query token with one
-// query head of the kv head's group, a row tile 16 * RT of them. A unit's keys
+// query head of the kv head's group, a row tile 8 * NT of them. A unit's keys
 // are cut into tiles of 32 tokens; tiles that no row sees are never read. All
 // units' tiles form one list that is cut into equal shares, one for each block,
 // so sequences of any lengths keep all blocks busy to the end. A unit that a
@@ -14,14 +14,19 @@
 // fourth tile of the share and has its own pipeline of cp.async stages. Which
 // bytes of a tile a lane copies is chosen so that it is the lane that uses them:
 // the contraction's order is free, so a lane's 16 bytes of a K row are the four
-// k positions of four MMA steps, and its 16 bytes of a V row are one column of 16
-// output tiles. No barrier, shared-memory transpose or bank conflict comes in.
+// k positions of four MMA steps, and its 16 bytes of a V row are one row of each
+// of 16 half output tiles. No barrier, shared-memory transpose or bank conflict
+// comes in.
 //
-// Codes become halves exactly (e4m3 by cvt, int8 by byte permutes); q, scaled by
+// The products are S^T = K q^T and O^T = V^T P^T: tokens and then columns of V are
+// the 16 rows of mma.sync m16n8k16, the query rows its 8 columns. A decoded token
+// has few rows, so this wastes less of the unit, and half the registers, of the
+// other order. P^T goes from the first product's result to the second's operand
+// by movmatrix. Codes become halves exactly (e4m3 by cvt, int8 by byte permutes); q, scaled by
 // a power of two for each row, becomes halves exactly down to 2^-28 of the row's
-// largest value. The matrix unit is mma.sync m16n8k16 with fp32 accumulation:
-// eight or sixteen rows against a tile are some 5% of its rate here, and tcgen05
-// takes 8-bit operands only in pairs, which would round q and P to 8 bits.
+// largest value. tcgen05 takes 8-bit operands only in pairs, which would round q
+// and P to 8 bits, and 16-bit ones from shared or tensor memory, which would cost
+// a write of every converted tile; eight rows need no such rate.
 //
 // Softmax in base 2 with two running maxima for each row: m of the scores, for
 // the sum l, and mo of score + log2(v_scale), for O, so that P * v_scale, a half,
@@ -49,8 +54,8 @@ struct PagedParams {
     const int32_t* cu;  // NULL: one token a sequence
     __nv_bfloat16* out;
     float* lse;       // [Hq, T]
-    float* part_o;    // [2 * blocks][16 * RT][D]
-    float* part_m;    // [2 * blocks][16 * RT][4]: m, mo, l
+    float* part_o;    // [2 * blocks][8 * NT][D]
+    float* part_m;    // [2 * blocks][8 * NT][4]: m, mo, l
     int32_t* heads_of_parts;  // [blocks][8]: a cut unit that begins in this block
     const float* slopes;
     int64_t T;
@@ -60,20 +65,20 @@ struct PagedParams {
     int* status;
 };
 
-template <int D>
+// Up to 32 registers of O a thread (NT * D <= 128): three blocks an SM with 16 KB of
+// stages a warp; more: two blocks, 24 KB a warp.
+template <int D, int NT>
 struct PagedStage {
+    static constexpr int kBlocks = NT * D > 128 ? 2 : 3;  // of an SM
     static constexpr int kK = kTileTokens * D, kV = kTileTokens * D;
     static constexpr int kBytes = kK + kV + 16;  // and the page scales: k, k, v, v
-    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kStages = (kBlocks == 2 ? 3 : 2) * (128 / D);
     static constexpr int kWarpBytes = kStages * kBytes;
-    static constexpr int kSmem = kPagedWarps * kWarpBytes;
+    static constexpr int kPitch = D + 4;  // floats of a row where the warps' parts meet
+    static constexpr int kMerge = kPagedWarps * 8 * NT * (kPitch + 4) * 4;
+    static constexpr int kQ = kPagedWarps * kWarpBytes > kMerge ? kPagedWarps * kWarpBytes : kMerge;
+    static constexpr int kSmem = kQ + (NT > 2 ? NT * (D / 16) * 256 : 0);  // NT = 4: q's fragments, too
 };
-
-// Dynamic shared memory of one block: the stages and, for RT = 2, q's fragments.
-template <int D, int RT>
-constexpr int paged_smem() {
-    return PagedStage<D>::kSmem + (RT > 1 ? RT * (D / 16) * 512 : 0);
-}
 
 __device__ __forceinline__ uint32_t shared_addr(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -103,15 +108,14 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
     return r;
 }
-__device__ __forceinline__ float lds32f(uint32_t a) {
-    float r;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(a));
+__device__ __forceinline__ float4 lds128f(uint32_t a) {
+    float4 r;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "r"(a));
     return r;
 }
 
 __device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -123,16 +127,34 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// Codes 0, 1 (LOW) or 2, 3 of a word as halves. The int8 codes come with their
-// top bit flipped (u = code + 128): the half 0x6400 | u is 1024 + u.
-template <bool INT8, bool LOW>
-__device__ __forceinline__ uint32_t halves_of(uint32_t w) {
+// A word's codes 0, 1 as the halves lo and codes 2, 3 as hi. The int8 codes come
+// with their top bit flipped (u = code + 128): the half 0x6400 | u is 1024 + u.
+template <bool INT8>
+__device__ __forceinline__ void halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
     if (INT8) {
-        const uint32_t x = __byte_perm(w, 0x64646464u, LOW ? 0x4140 : 0x4342);
-        const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0x6480)));
-        return *reinterpret_cast<const uint32_t*>(&y);
+        const uint32_t x = __byte_perm(w, 0x64646464u, 0x4140), y = __byte_perm(w, 0x64646464u, 0x4342);
+        const __half2 off = __half2half2(__ushort_as_half(0x6480));
+        const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&x), off);
+        const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&y), off);
+        lo = *reinterpret_cast<const uint32_t*>(&a);
+        hi = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
     }
-    return e4m3x2_to_half2(LOW ? w & 0xFFFFu : w >> 16);
+}
+
+// The transpose of an 8 x 8 matrix of halves held in the warp's fragment layout.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 template <bool INT8>
@@ -228,14 +250,15 @@ __device__ __forceinline__ int64_t paged_weight(const PagedParams& p, const Page
     return row_tiles * p.c.heads * max(tiles, 1);
 }
 
-template <int D, bool INT8, int RT, bool MODS>
-__global__ void __launch_bounds__(kPagedThreads, 2) paged_attention_kernel(const __grid_constant__ PagedParams p,
-                                                                           const __grid_constant__ MaskDnf dnf) {
-    using Stage = PagedStage<D>;
+template <int D, bool INT8, int NT, bool MODS>
+__global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
+    paged_attention_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ MaskDnf dnf) {
+    using Stage = PagedStage<D, NT>;
     constexpr int kSteps = D / 16;   // MMA steps over the head dimension
     constexpr int kChunks = D / 64;  // 16-byte pieces of a K row that one lane holds
-    constexpr int kOut = D / 8;      // output tiles of 8 columns
-    constexpr int kRows = 16 * RT;
+    constexpr int kOut = D / 16;     // output tiles of 16 columns of V
+    constexpr int kRows = 8 * NT;
+    constexpr bool kQShared = NT > 2;  // q's fragments in shared memory, not registers
     constexpr float kLog2e = 1.4426950408889634f;
     constexpr float kLn2 = 0.6931471805599453f;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -243,7 +266,6 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_attention_kernel(const
     __shared__ long long s_off;
     __shared__ int s_i;
     __shared__ PagedSeqShared s_seq;
-    __shared__ float s_qscale[kRows];
     const KvCache& c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -251,12 +273,24 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_attention_kernel(const
     // ---- this block's share of all tiles
     const int per_thread = (p.n + kPagedThreads - 1) / kPagedThreads;
     const int i_lo = min(p.n, tid * per_thread), i_hi = min(p.n, i_lo + per_thread);
+    auto describe = [&](const PagedSeq& s) {  // what the whole block needs of a sequence
+        s_seq.s = s;
+        s_seq.tiles = seen_tiles(dnf, s.len - s.count, s.len - 1, s.len, s_seq.first, s_seq.last, &s_seq.runs);
+        s_seq.weight = paged_weight(p, s, s_seq.tiles, kRows);
+        for (int x = 0; x < dnf.n_terms; ++x) {
+            int64_t unused;
+            term_interval(dnf, x, s.len - 1, 0, s.len - 1, 0, 0, s_seq.clean_lo[x], unused);
+            term_interval(dnf, x, s.len - s.count, 0, s.len - 1, 0, 0, unused, s_seq.clean_hi[x]);
+        }
+    };
     long long mine = 0;
+    PagedSeq own;  // the thread's sequence, where there is one for each thread at most
+    own.count = 0;
     for (int i = i_lo; i < i_hi; ++i) {
-        const PagedSeq s = paged_seq(p, i);
+        own = paged_seq(p, i);
         int first[kMaxTerms], last[kMaxTerms], runs;
-        const int tiles = seen_tiles(dnf, s.len - s.count, s.len - 1, s.len, first, last, &runs);
-        mine += paged_weight(p, s, tiles, kRows);
+        const int tiles = seen_tiles(dnf, own.len - own.count, own.len - 1, own.len, first, last, &runs);
+        mine += paged_weight(p, own, tiles, kRows);
     }
     long long incl = mine;
 #pragma unroll
@@ -272,35 +306,41 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_attention_kernel(const
         all += s_scan[w];
         if (w < warp) before += s_scan[w];
     }
-    long long share = (all + gridDim.x - 1) / gridDim.x;
+    long long share = all <= static_cast<long long>(0xFFFFFFFFu - gridDim.x)
+                          ? (static_cast<uint32_t>(all) + gridDim.x - 1) / gridDim.x
+                          : (all + gridDim.x - 1) / gridDim.x;
     if (share < p.min_share) share = p.min_share;
     const long long begin = share * blockIdx.x, end = min(all, begin + share);
     if (begin < end && before <= begin && begin < before + mine) {
         long long off = begin - before;
-        for (int i = i_lo; i < i_hi; ++i) {
-            const PagedSeq s = paged_seq(p, i);
-            int first[kMaxTerms], last[kMaxTerms], runs;
-            const int tiles = seen_tiles(dnf, s.len - s.count, s.len - 1, s.len, first, last, &runs);
-            const long long w = paged_weight(p, s, tiles, kRows);
-            if (off < w) {
-                s_i = i;
-                s_off = off;
-                break;
+        int i = i_lo;
+        if (per_thread > 1) {
+            for (; i < i_hi; ++i) {
+                own = paged_seq(p, i);
+                int first[kMaxTerms], last[kMaxTerms], runs;
+                const int tiles = seen_tiles(dnf, own.len - own.count, own.len - 1, own.len, first, last, &runs);
+                const long long w = paged_weight(p, own, tiles, kRows);
+                if (off < w) break;
+                off -= w;
             }
-            off -= w;
         }
+        s_i = i;
+        s_off = off;
+        describe(own);
     }
     if (tid == 0) p.heads_of_parts[blockIdx.x * 8] = 0;
     // rows behind the last sequence belong to none: they see nothing
     if (p.cu != nullptr) {
         const int64_t used = max(0, min(__ldg(p.cu + p.n), static_cast<int>(p.T)));
-        const int64_t stride = static_cast<int64_t>(gridDim.x) * kPagedThreads;
-        const int64_t rest = (p.T - used) * p.Hq;
-        uint4* o = reinterpret_cast<uint4*>(p.out + used * p.Hq * D);
-        for (int64_t x = static_cast<int64_t>(blockIdx.x) * kPagedThreads + tid; x < rest * (D / 8); x += stride)
-            o[x] = make_uint4(0, 0, 0, 0);
-        for (int64_t x = static_cast<int64_t>(blockIdx.x) * kPagedThreads + tid; x < rest; x += stride)
-            p.lse[x / (p.T - used) * p.T + used + x % (p.T - used)] = -INFINITY;
+        if (used < p.T) {
+            const int64_t stride = static_cast<int64_t>(gridDim.x) * kPagedThreads;
+            const int64_t rest = (p.T - used) * p.Hq;
+            uint4* o = reinterpret_cast<uint4*>(p.out + used * p.Hq * D);
+            for (int64_t x = static_cast<int64_t>(blockIdx.x) * kPagedThreads + tid; x < rest * (D / 8); x += stride)
+                o[x] = make_uint4(0, 0, 0, 0);
+            for (int64_t x = static_cast<int64_t>(blockIdx.x) * kPagedThreads + tid; x < rest; x += stride)
+                p.lse[x / (p.T - used) * p.T + used + x % (p.T - used)] = -INFINITY;
+        }
     }
     __syncthreads();
     if (begin >= end) return;
@@ -309,42 +349,40 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_attention_kernel(const
     long long off = s_off, left = end - begin;
     bool first_segment = true;
     const uint32_t stages = shared_addr(smem) + warp * Stage::kWarpBytes;
+    const uint32_t lane_stage = stages + lane * 16, lane_v = stages + Stage::kK + lane * (D / 8);
     const int64_t head_bytes = static_cast<int64_t>(c.page) * D;
     const int64_t page_bytes = head_bytes * c.heads;
+    const uint8_t* const k_pool = c.k + static_cast<int64_t>(p.layer) * c.pages * page_bytes + g * D + 16 * t;
+    const uint8_t* const v_pool = c.v + static_cast<int64_t>(p.layer) * c.pages * page_bytes + 2 * t * D + g * (D / 8);
+    const float* const k_scales = c.k_scale + static_cast<int64_t>(p.layer) * c.pages * c.heads;
+    const float* const v_scales = c.v_scale + static_cast<int64_t>(p.layer) * c.pages * c.heads;
 
-    for (; left > 0 && i < p.n; ++i, off = 0) {
-        __syncthreads();
-        if (tid == 0) {
-            const PagedSeq s = paged_seq(p, i);
-            s_seq.s = s;
-            s_seq.tiles = seen_tiles(dnf, s.len - s.count, s.len - 1, s.len, s_seq.first, s_seq.last, &s_seq.runs);
-            s_seq.weight = paged_weight(p, s, s_seq.tiles, kRows);
-            for (int x = 0; x < dnf.n_terms; ++x) {
-                int64_t unused;
-                term_interval(dnf, x, s.len - 1, 0, s.len - 1, 0, 0, s_seq.clean_lo[x], unused);
-                term_interval(dnf, x, s.len - s.count, 0, s.len - 1, 0, 0, unused, s_seq.clean_hi[x]);
-            }
-        }
-        __syncthreads();
+    while (true) {
         const int64_t len = s_seq.s.len;
         const int count = s_seq.s.count;
         const int seen = s_seq.tiles, tiles = max(seen, 1);
         const int64_t weight = s_seq.weight;
         const int32_t* table = c.page_table + static_cast<int64_t>(max(s_seq.s.slot, 0)) * c.max_pages;
+        const int64_t rows_all = static_cast<int64_t>(count) * p.group;
+        int64_t unit = 0;
+        int t0 = 0;
+        if (off != 0) {
+            unit = off / tiles;
+            t0 = static_cast<int>(off - unit * tiles);
+        }
+        int64_t tile_row = unit / c.heads;
+        int head = static_cast<int>(unit - tile_row * c.heads);
 
         while (off < weight && left > 0) {
-            const int64_t unit = off / tiles;
-            const int t0 = static_cast<int>(off - unit * tiles);
             const int t1 = static_cast<int>(min(static_cast<long long>(tiles), t0 + left));
-            const int head = static_cast<int>(unit % c.heads);
-            const int64_t row0 = unit / c.heads * kRows;  // the unit's first row
-            const int64_t rows_all = static_cast<int64_t>(count) * p.group;
+            const int64_t row0 = tile_row * kRows;  // the unit's first row
+            const int64_t qi0 = rows_all < 0x7FFFFFFF ? static_cast<int64_t>(static_cast<uint32_t>(row0) / static_cast<uint32_t>(p.group))
+                                                      : row0 / p.group;
+            const int in_group = static_cast<int>(row0 - qi0 * p.group);  // row0 = qi0 * group + in_group
 
             // ---- pipeline over this warp's tiles
-            const uint8_t* k_head = c.k + static_cast<int64_t>(p.layer) * c.pages * page_bytes + head * head_bytes;
-            const uint8_t* v_head = c.v + static_cast<int64_t>(p.layer) * c.pages * page_bytes + head * head_bytes;
-            const float* k_scale = c.k_scale + static_cast<int64_t>(p.layer) * c.pages * c.heads + head;
-            const float* v_scale = c.v_scale + static_cast<int64_t>(p.layer) * c.pages * c.heads + head;
+            const uint8_t* const k_head = k_pool + head * head_bytes;
+            const uint8_t* const v_head = v_pool + head * head_bytes;
             int run = 0, run_base = 0;  // the run that the next tile to load lies in, and the tiles before it
             auto tile_of = [&](int ord) -> int64_t {  // first token of the unit's tile `ord`; -1: none
                 if (ord >= t1 || ord >= seen) return -1;
@@ -354,50 +392,57 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_attention_kernel(const
                 }
                 return static_cast<int64_t>(s_seq.first[run] + ord - run_base) * kTileTokens;
             };
-            auto page_at = [&](int64_t tok) -> int {  // page of a token; -1: behind the sequence, or a bad one
+            auto page_at = [&](int64_t tok) -> int {  // page of a token; -1: behind the sequence
                 if (tok < 0 || tok >= len) return -1;
                 return __ldg(table + (tok >> c.page_shift));
-            };
-            auto check_page = [&](int page) -> int {
-                if (page >= 0 && page < c.pages) return page;
-                return -1;
             };
             int next_ord = t0 + warp;
             int64_t next_tok = tile_of(next_ord);
             int next_a = page_at(next_tok), next_b = page_at(next_tok < 0 ? -1 : next_tok + 16);
             auto issue = [&](int stage) {
-                const uint32_t st = stages + stage * Stage::kBytes;
+                const uint32_t st = stage * Stage::kBytes;
                 if (next_tok >= 0) {
-                    const int pa = check_page(next_a), pb = check_page(next_b);
-                    if ((pa < 0 || (pb < 0 && next_tok + 16 < len)) && lane == 0)
-                        set_status(p.status, BSMT_ERR_DEVICE_BOUNDS);
-                    const int in_page = static_cast<int>(next_tok & (c.page - 1));
-                    const int in_b = static_cast<int>((next_tok + 16) & (c.page - 1));
-                    const int64_t base_a = pa < 0 ? 0 : pa * page_bytes + static_cast<int64_t>(in_page) * D;
-                    const int64_t base_b = pb < 0 ? 0 : pb * page_bytes + static_cast<int64_t>(in_b) * D;
-                    const int have = static_cast<int>(min(static_cast<int64_t>(kTileTokens), len - next_tok));
+                    int pa = next_a, pb = next_b;
+                    const bool ok_a = pa >= 0 && pa < c.pages, ok_b = pb >= 0 && pb < c.pages;
+                    const int in_a = static_cast<int>(next_tok) & (c.page - 1), in_b = (static_cast<int>(next_tok) + 16) & (c.page - 1);
+                    if (!ok_a) pa = 0;
+                    if (!ok_b) pb = 0;
+                    const int64_t base_a = pa * page_bytes + in_a * D, base_b = pb * page_bytes + in_b * D;
+                    if (ok_a && ok_b && next_tok + kTileTokens <= len) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const bool there = 8 * j + g < have && (j < 2 ? pa : pb) >= 0;
-                        const uint8_t* src = k_head + (j < 2 ? base_a : base_b) + ((j & 1) * 8 + g) * D + 16 * t;
+                        for (int j = 0; j < 4; ++j)
 #pragma unroll
-                        for (int x = 0; x < kChunks; ++x)
-                            cp_async<16>(st + (j * kChunks + x) * 512 + lane * 16, src + 64 * x, there);
-                    }
+                            for (int x = 0; x < kChunks; ++x)
+                                cp_async<16>(lane_stage + st + (j * kChunks + x) * 512,
+                                             k_head + (j < 2 ? base_a : base_b) + (j & 1) * 8 * D + 64 * x, true);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                        for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const int row = 2 * t + (x & 1) + 8 * (x >> 1);
-                            const bool there = 16 * h + row < have && (h ? pb : pa) >= 0;
-                            const uint8_t* src = v_head + (h ? base_b : base_a) + row * D + g * (D / 8);
-                            cp_async<D / 8>(st + Stage::kK + ((h * 4 + x) * 32 + lane) * (D / 8), src, there);
-                        }
+                            for (int x = 0; x < 4; ++x)
+                                cp_async<D / 8>(lane_v + st + (h * 4 + x) * 32 * (D / 8),
+                                                v_head + (h ? base_b : base_a) + ((x & 1) + 8 * (x >> 1)) * D, true);
+                    } else {
+                        // the sequence's last tile, or a bad page: rows that are not there are zeros
+                        const int have = static_cast<int>(min(static_cast<int64_t>(kTileTokens), len - next_tok));
+                        if ((!ok_a || (!ok_b && have > 16)) && lane == 0) set_status(p.status, BSMT_ERR_DEVICE_BOUNDS);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int x = 0; x < kChunks; ++x)
+                                cp_async<16>(lane_stage + st + (j * kChunks + x) * 512,
+                                             k_head + (j < 2 ? base_a : base_b) + (j & 1) * 8 * D + 64 * x,
+                                             8 * j + g < have && (j < 2 ? ok_a : ok_b));
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                cp_async<D / 8>(lane_v + st + (h * 4 + x) * 32 * (D / 8),
+                                                v_head + (h ? base_b : base_a) + ((x & 1) + 8 * (x >> 1)) * D,
+                                                16 * h + 2 * t + (x & 1) + 8 * (x >> 1) < have && (h ? ok_b : ok_a));
                     }
                     if (lane < 4) {
-                        const int page = (lane & 1) ? pb : pa;
-                        const float* src = ((lane & 2) ? v_scale : k_scale) + static_cast<int64_t>(max(page, 0)) * c.heads;
-                        cp_async<4>(st + Stage::kK + Stage::kV + lane * 4, src, page >= 0);
+                        const float* src = ((lane & 2) ? v_scales : k_scales) + static_cast<int64_t>((lane & 1) ? pb : pa) * c.heads + head;
+                        cp_async<4>(stages + st + Stage::kK + Stage::kV + lane * 4, src, (lane & 1) ? ok_b : ok_a);
                     }
                 }
                 cp_async_commit();
@@ -413,76 +458,81 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_attention_kernel(const
                 issue(x);
             }
 
-            // ---- q: rows g and g + 8 of each row tile, in halves
-            uint32_t qf[RT > 1 ? 1 : kSteps][4];
-            float qs[RT][2];
-            int64_t pos[RT][2];
-            float slope[RT][2];
-            bool valid[RT][2];
-            const uint32_t q_smem = shared_addr(smem) + Stage::kSmem;
+            // ---- q: row g of each 8, in halves; what the softmax needs of rows 2 t and 2 t + 1
+            uint32_t qf[kQShared ? 1 : NT][kSteps][2];
+            float qs[NT][2], slope[NT][2];
+            int64_t pos[NT][2];
+            const uint32_t q_smem = shared_addr(smem) + Stage::kQ + lane * 8;
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
+            for (int r = 0; r < NT; ++r) {
+                const int row = 8 * r + g;
+                const bool valid = row0 + row < rows_all;
+                const int up_q = static_cast<int>(static_cast<uint32_t>(in_group + row) / static_cast<uint32_t>(p.group));
+                const int64_t qi = valid ? qi0 + up_q : 0;
+                const int hq = head * p.group + (valid ? in_group + row - up_q * p.group : 0);
+                uint32_t w[kChunks][8];
+                const uint4* src = reinterpret_cast<const uint4*>(p.q + ((s_seq.s.q0 + qi) * p.Hq + hq) * D + 16 * t);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int64_t row = row0 + 16 * r + 8 * h + g;
-                    valid[r][h] = row < rows_all;
-                    const int64_t qi = valid[r][h] ? row / p.group : 0;
-                    const int hq = head * p.group + static_cast<int>(valid[r][h] ? row - qi * p.group : 0);
-                    pos[r][h] = len - count + qi;
-                    slope[r][h] = 0.f;
-                    if (MODS && p.alibi)
-                        slope[r][h] = p.slopes != nullptr
-                                          ? __ldg(p.slopes + hq)
-                                          : exp2f(-8.f * static_cast<float>(p.alibi_h0 + hq + 1) / static_cast<float>(p.alibi_heads));
-                    uint32_t w[kChunks][8];
-                    const uint4* src = reinterpret_cast<const uint4*>(p.q + ((s_seq.s.q0 + qi) * p.Hq + hq) * D + 16 * t);
+                for (int x = 0; x < kChunks; ++x) {
+                    const uint4 a = valid ? __ldg(src + 8 * x) : make_uint4(0, 0, 0, 0);
+                    const uint4 b = valid ? __ldg(src + 8 * x + 1) : make_uint4(0, 0, 0, 0);
+                    w[x][0] = a.x, w[x][1] = a.y, w[x][2] = a.z, w[x][3] = a.w;
+                    w[x][4] = b.x, w[x][5] = b.y, w[x][6] = b.z, w[x][7] = b.w;
+                }
+                uint32_t most = 0;
 #pragma unroll
-                    for (int x = 0; x < kChunks; ++x) {
-                        const uint4 a = valid[r][h] ? __ldg(src + 8 * x) : make_uint4(0, 0, 0, 0);
-                        const uint4 b = valid[r][h] ? __ldg(src + 8 * x + 1) : make_uint4(0, 0, 0, 0);
-                        w[x][0] = a.x, w[x][1] = a.y, w[x][2] = a.z, w[x][3] = a.w;
-                        w[x][4] = b.x, w[x][5] = b.y, w[x][6] = b.z, w[x][7] = b.w;
+                for (int x = 0; x < kChunks; ++x)
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {
+                        const uint32_t a = w[x][y] & 0x7FFFu, b = w[x][y] >> 16 & 0x7FFFu;
+                        most = max(most, max(a < 0x7F80u ? a : 0u, b < 0x7F80u ? b : 0u));
                     }
-                    uint32_t most = 0;
+                most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+                most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+                // largest value to [2^14, 2^15): the row's small values keep their bits, too
+                const int e = max(static_cast<int>(most >> 7) - 127, -100) - 14;
+                const float row_scale = exp2i(e) * p.scale * (MODS ? 1.f : kLog2e);
+                const float up = exp2i(-e);
 #pragma unroll
-                    for (int x = 0; x < kChunks; ++x)
+                for (int x = 0; x < kChunks; ++x)
 #pragma unroll
-                        for (int y = 0; y < 8; ++y) {
-                            const uint32_t a = w[x][y] & 0x7FFFu, b = w[x][y] >> 16 & 0x7FFFu;
-                            most = max(most, max(a < 0x7F80u ? a : 0u, b < 0x7F80u ? b : 0u));
+                    for (int y = 0; y < 4; ++y) {
+                        uint32_t u[2];
+#pragma unroll
+                        for (int z = 0; z < 2; ++z)
+                            u[z] = pack_half2(__uint_as_float(w[x][2 * y + z] << 16) * up,
+                                              __uint_as_float(w[x][2 * y + z] & 0xFFFF0000u) * up);
+                        if (!kQShared) {
+                            qf[r][4 * x + y][0] = u[0], qf[r][4 * x + y][1] = u[1];
+                        } else if (warp == r) {
+                            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(q_smem + (r * kSteps + 4 * x + y) * 256),
+                                         "r"(u[0]), "r"(u[1])
+                                         : "memory");
                         }
-                    most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-                    most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-                    // largest value to [2^14, 2^15): the row's small values keep their bits, too
-                    const int e = max(static_cast<int>(most >> 7) - 127, -100) - 14;
-                    qs[r][h] = exp2i(e) * p.scale * (MODS ? 1.f : kLog2e);
-                    const float up = exp2i(-e);
+                    }
 #pragma unroll
-                    for (int x = 0; x < kChunks; ++x)
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) {
-                            const __half2 v = __floats2half2_rn(__uint_as_float(w[x][y] << 16) * up,
-                                                                __uint_as_float(w[x][y] & 0xFFFF0000u) * up);
-                            const uint32_t u = *reinterpret_cast<const uint32_t*>(&v);
-                            // step 4 x + y / 2: a[0], a[1] rows g, g + 8 of the first pair, a[2], a[3] of the second
-                            if (RT == 1)
-                                qf[4 * x + y / 2][h + 2 * (y & 1)] = u;
-                            else if (warp == r)
-                                asm volatile("st.shared.u32 [%0], %1;" ::"r"(q_smem + ((r * kSteps + 4 * x + y / 2) * 32 + lane) * 16 +
-                                                                             (h + 2 * (y & 1)) * 4),
-                                             "r"(u)
-                                             : "memory");
-                        }
+                for (int y = 0; y < 2; ++y) {
+                    const int col = 8 * r + 2 * t + y;
+                    const int up_c = static_cast<int>(static_cast<uint32_t>(in_group + col) / static_cast<uint32_t>(p.group));
+                    qs[r][y] = __shfl_sync(0xFFFFFFFFu, row_scale, (2 * t + y) * 4);
+                    pos[r][y] = len - count + qi0 + up_c;
+                    slope[r][y] = 0.f;
+                    if (MODS && p.alibi && row0 + col < rows_all) {
+                        const int h = head * p.group + in_group + col - up_c * p.group;
+                        slope[r][y] = p.slopes != nullptr
+                                          ? __ldg(p.slopes + h)
+                                          : exp2f(-8.f * static_cast<float>(p.alibi_h0 + h + 1) / static_cast<float>(p.alibi_heads));
+                    }
                 }
             }
-            if (RT > 1) __syncthreads();
+            if (kQShared) __syncthreads();
 
-            float o[RT][kOut][4];
-            float m[RT][2], mo[RT][2], l[RT][2];
+            float o[NT][kOut][4];
+            float m[NT][2], mo[NT][2], l[NT][2];
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
+            for (int r = 0; r < NT; ++r) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) m[r][h] = mo[r][h] = -INFINITY, l[r][h] = 0.f;
+                for (int y = 0; y < 2; ++y) m[r][y] = mo[r][y] = -INFINITY, l[r][y] = 0.f;
 #pragma unroll
                 for (int x = 0; x < kOut; ++x)
 #pragma unroll
@@ -494,136 +544,149 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_attention_kernel(const
                 cp_async_wait<Stage::kStages - 1>();
                 __syncwarp();
                 const int64_t tok = tok_q[0];
-                const uint32_t st = stages + stage * Stage::kBytes;
+                const uint32_t st = stage * Stage::kBytes;
                 if (tok >= 0) {
-                    float s[RT][4][4];
+                    // s[r][h][2 z + y]: token 16 h + 8 z + g, row 8 r + 2 t + y
+                    float s[NT][2][4];
 #pragma unroll
-                    for (int r = 0; r < RT; ++r)
+                    for (int r = 0; r < NT; ++r)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
+                        for (int h = 0; h < 2; ++h)
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) s[r][j][y] = 0.f;
+                            for (int y = 0; y < 4; ++y) s[r][h][y] = 0.f;
 #pragma unroll
                     for (int x = 0; x < kChunks; ++x) {
-                        uint4 kw[4];
+                        uint32_t kw[4][4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) kw[j] = lds128(st + (j * kChunks + x) * 512 + lane * 16);
+                        for (int j = 0; j < 4; ++j) {
+                            const uint4 v = lds128(lane_stage + st + (j * kChunks + x) * 512);
+                            kw[j][0] = flip<INT8>(v.x), kw[j][1] = flip<INT8>(v.y), kw[j][2] = flip<INT8>(v.z), kw[j][3] = flip<INT8>(v.w);
+                        }
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
-                            uint32_t a[RT][4];
+                            uint32_t b[NT][2];
 #pragma unroll
-                            for (int r = 0; r < RT; ++r) {
-                                if (RT == 1) {
-#pragma unroll
-                                    for (int z = 0; z < 4; ++z) a[r][z] = qf[4 * x + y][z];
+                            for (int r = 0; r < NT; ++r) {
+                                if (!kQShared) {
+                                    b[r][0] = qf[r][4 * x + y][0], b[r][1] = qf[r][4 * x + y][1];
                                 } else {
-                                    const uint4 v = lds128(q_smem + ((r * kSteps + 4 * x + y) * 32 + lane) * 16);
-                                    a[r][0] = v.x, a[r][1] = v.y, a[r][2] = v.z, a[r][3] = v.w;
+                                    const uint2 v = lds64(q_smem + (r * kSteps + 4 * x + y) * 256);
+                                    b[r][0] = v.x, b[r][1] = v.y;
                                 }
                             }
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint32_t w = flip<INT8>(y == 0 ? kw[j].x : y == 1 ? kw[j].y : y == 2 ? kw[j].z : kw[j].w);
-                                const uint32_t b0 = halves_of<INT8, true>(w), b1 = halves_of<INT8, false>(w);
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t a[4];  // tokens g, g + 8; codes 0, 1 then 2, 3
+                                halves<INT8>(kw[2 * h][y], a[0], a[2]);
+                                halves<INT8>(kw[2 * h + 1][y], a[1], a[3]);
 #pragma unroll
-                                for (int r = 0; r < RT; ++r) mma16816(s[r][j], a[r], b0, b1);
+                                for (int r = 0; r < NT; ++r) mma16816(s[r][h], a, b[r][0], b[r][1]);
                             }
                         }
                     }
-                    const uint32_t sc = st + Stage::kK + Stage::kV;
-                    const float ks[2] = {lds32f(sc), lds32f(sc + 4)}, vs[2] = {lds32f(sc + 8), lds32f(sc + 12)};
+                    const uint32_t sc = stages + st + Stage::kK + Stage::kV;
+                    const float4 scales = lds128f(sc);
+                    const float ks[2] = {scales.x, scales.y}, vs[2] = {scales.z, scales.w};
                     const float ev[2] = {__log2f(fmaxf(vs[0], 0x1p-126f)), __log2f(fmaxf(vs[1], 0x1p-126f))};
 
                     // which keys the rows see
                     bool clean = false;
                     for (int x = 0; x < dnf.n_terms; ++x)
                         clean = clean || (s_seq.clean_lo[x] <= tok && tok + kTileTokens - 1 <= s_seq.clean_hi[x]);
-                    uint32_t bits[RT][2];
+                    uint32_t bits[NT][2];
+                    if (!clean) {
 #pragma unroll
-                    for (int r = 0; r < RT; ++r)
+                        for (int r = 0; r < NT; ++r)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            bits[r][h] = 0xFFFFFFFFu;
-                            if (!clean) {
-                                bits[r][h] = 0;
+                            for (int y = 0; y < 2; ++y) {
+                                bits[r][y] = 0;
                                 for (int x = 0; x < dnf.n_terms; ++x) {
                                     int64_t lo, hi;
-                                    term_interval(dnf, x, pos[r][h], 0, len - 1, 0, 0, lo, hi);
-                                    bits[r][h] |= range_bits(lo, hi, tok);
+                                    term_interval(dnf, x, pos[r][y], 0, len - 1, 0, 0, lo, hi);
+                                    bits[r][y] |= range_bits(lo, hi, tok);
                                 }
                             }
-                        }
+                    }
+                    if (MODS) {
+                        const int rel = static_cast<int>(tok - pos[0][0]) + g;
+#pragma unroll
+                        for (int r = 0; r < NT; ++r)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const int y = e & 1;
+                                    float z = s[r][h][e] * (qs[r][y] * ks[h]);
+                                    const float bias = slope[r][y] * static_cast<float>(rel + 16 * h + 8 * (e >> 1) -
+                                                                                        static_cast<int>(pos[r][y] - pos[0][0]));
+                                    if (p.alibi_first) z += bias;
+                                    // cap * tanh(z / cap), tanh(u) = 1 - 2 / (exp(2 u) + 1)
+                                    if (p.softcap) z = p.cap * (1.f - __fdividef(2.f, exp2_fast(z * (2.f * kLog2e / p.cap)) + 1.f));
+                                    if (!p.alibi_first) z += bias;
+                                    s[r][h][e] = z * kLog2e;
+                                }
+                    }
+                    if (!clean) {
+#pragma unroll
+                        for (int r = 0; r < NT; ++r)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (!(bits[r][e & 1] >> (16 * h + 8 * (e >> 1) + g) & 1u)) s[r][h][e] = -INFINITY;
+                    }
 
-                    uint32_t pa[RT][2][4];
+                    uint32_t pb[NT][2][2];
 #pragma unroll
-                    for (int r = 0; r < RT; ++r) {
-                        float top[2][2];  // [row][16-token half]
+                    for (int r = 0; r < NT; ++r) {
+                        float ao[2], al[2], ref[2], f[2][2], cf[2][2];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            top[h][0] = top[h][1] = -INFINITY;
+                        for (int y = 0; y < 2; ++y) {
+                            float top[2];  // of each 16 tokens
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                                for (int y = 0; y < 2; ++y) {
-                                    float z = s[r][j][2 * h + y] * (qs[r][h] * ks[j >> 1]);
-                                    if (MODS) {
-                                        const float bias =
-                                            slope[r][h] * static_cast<float>(static_cast<int>(tok + 8 * j + 2 * t + y - pos[r][h]));
-                                        if (p.alibi_first) z += bias;
-                                        // cap * tanh(z / cap), tanh(u) = 1 - 2 / (exp(2 u) + 1)
-                                        if (p.softcap)
-                                            z = p.cap * (1.f - __fdividef(2.f, exp2_fast(z * (2.f * kLog2e / p.cap)) + 1.f));
-                                        if (!p.alibi_first) z += bias;
-                                        z *= kLog2e;
-                                    }
-                                    if (!(bits[r][h] >> (8 * j + 2 * t + y) & 1u)) z = -INFINITY;
-                                    s[r][j][2 * h + y] = z;
-                                    top[h][j >> 1] = fmaxf(top[h][j >> 1], z);
-                                }
-                        }
-                        float al[2], ao[2], cf[2][2], ref[2];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                top[h][x] = fmaxf(top[h][x], __shfl_xor_sync(0xFFFFFFFFu, top[h][x], 1));
-                                top[h][x] = fmaxf(top[h][x], __shfl_xor_sync(0xFFFFFFFFu, top[h][x], 2));
+                            for (int h = 0; h < 2; ++h) {
+                                // a score is s * f, f > 0 (a scale of 0 belongs to codes of 0)
+                                f[y][h] = MODS ? 1.f : fmaxf(qs[r][y] * ks[h], 1e-37f);
+                                top[h] = fmaxf(s[r][h][y], s[r][h][2 + y]);
+                                top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], 4));
+                                top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], 8));
+                                top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], 16));
+                                if (!MODS) top[h] *= f[y][h];
                             }
-                            const float mn = fmaxf(m[r][h], fmaxf(top[h][0], top[h][1]));
-                            const float mon = fmaxf(mo[r][h], fmaxf(top[h][0] + ev[0], top[h][1] + ev[1]));
-                            ref[h] = mn == -INFINITY ? 0.f : mn;
+                            const float mn = fmaxf(m[r][y], fmaxf(top[0], top[1]));
+                            const float mon = fmaxf(mo[r][y], fmaxf(top[0] + ev[0], top[1] + ev[1]));
+                            ref[y] = mn == -INFINITY ? 0.f : mn;
                             const float refo = mon == -INFINITY ? 0.f : mon;
-                            al[h] = exp2_fast(m[r][h] - ref[h]);
-                            ao[h] = exp2_fast(mo[r][h] - refo);
-                            const float shift = exp2_fast(ref[h] - refo);
-                            cf[h][0] = vs[0] * shift;
-                            cf[h][1] = vs[1] * shift;
-                            if (mn == -INFINITY) cf[h][0] = cf[h][1] = 0.f;
-                            m[r][h] = mn;
-                            mo[r][h] = mon;
+                            al[y] = exp2_fast(m[r][y] - ref[y]);
+                            ao[y] = exp2_fast(mo[r][y] - refo);
+                            const float shift = mn == -INFINITY ? 0.f : exp2_fast(ref[y] - refo);
+                            cf[y][0] = vs[0] * shift;
+                            cf[y][1] = vs[1] * shift;
+                            m[r][y] = mn;
+                            mo[r][y] = mon;
                         }
                         if (__any_sync(0xFFFFFFFFu, ao[0] != 1.f || ao[1] != 1.f)) {
 #pragma unroll
-                            for (int x = 0; x < kOut; ++x) {
-                                o[r][x][0] *= ao[0];
-                                o[r][x][1] *= ao[0];
-                                o[r][x][2] *= ao[1];
-                                o[r][x][3] *= ao[1];
-                            }
+                            for (int x = 0; x < kOut; ++x)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) o[r][x][e] *= ao[e & 1];
                         }
+                        float sum[2] = {0.f, 0.f};
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float sum = 0.f;
+                        for (int h = 0; h < 2; ++h)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float a = exp2_fast(s[r][j][2 * h] - ref[h]), b = exp2_fast(s[r][j][2 * h + 1] - ref[h]);
-                                sum += a + b;
+                            for (int z = 0; z < 2; ++z) {
+                                float e[2];
+#pragma unroll
+                                for (int y = 0; y < 2; ++y) {
+                                    e[y] = exp2_fast(MODS ? s[r][h][2 * z + y] - ref[y] : fmaf(s[r][h][2 * z + y], f[y][h], -ref[y]));
+                                    sum[y] += e[y];
+                                }
                                 // P to 11 bits: an error of 2^-12 of each term, below the output's bf16 rounding
-                                const __half2 v = __floats2half2_rn(a * cf[h][j >> 1], b * cf[h][j >> 1]);
-                                pa[r][j >> 1][h + 2 * (j & 1)] = *reinterpret_cast<const uint32_t*>(&v);
+                                pb[r][h][z] = transpose8x8(pack_half2(e[0] * cf[0][h], e[1] * cf[1][h]));
                             }
-                            l[r][h] = l[r][h] * al[h] + sum;
-                        }
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) l[r][y] = l[r][y] * al[y] + sum[y];
                     }
 
 #pragma unroll
@@ -631,7 +694,7 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_attention_kernel(const
                         uint32_t vw[4][D / 32];
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            const uint32_t a = st + Stage::kK + ((h * 4 + x) * 32 + lane) * (D / 8);
+                            const uint32_t a = lane_v + st + (h * 4 + x) * 32 * (D / 8);
                             if (D == 128) {
                                 const uint4 v = lds128(a);
                                 vw[x][0] = v.x, vw[x][1] = v.y, vw[x][D / 32 - 2] = v.z, vw[x][D / 32 - 1] = v.w;
@@ -640,67 +703,65 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_attention_kernel(const
                                 vw[x][0] = v.x, vw[x][1] = v.y;
                             }
                         }
+                        // 4 x 4 bytes: token-major words -> for each column of V its four tokens; tile 2 w + b has
+                        // columns 4 w + 2 b (rows g) and 4 w + 2 b + 1 (rows g + 8) of the lane's D / 8
+                        auto columns = [&](const uint32_t w0, const uint32_t w1, const uint32_t w2, const uint32_t w3, int b, uint32_t a[4]) {
+                            halves<INT8>(__byte_perm(w0, w1, b ? 0x7362 : 0x5140), a[0], a[1]);
+                            halves<INT8>(__byte_perm(w2, w3, b ? 0x7362 : 0x5140), a[2], a[3]);
+                        };
                         if (!INT8 && !clean) {
                             // 0 * NaN: a NaN code that some row does not see must not reach that row. Rare
                             // (NaN values in a tile on the mask's edge): the codes become 0 here, and rows
-                            // that see one get NaN from a product of visibility and NaN indicators.
+                            // that see one get NaN from a product of NaN indicators and visibility.
                             uint32_t found = 0;
 #pragma unroll
                             for (int x = 0; x < 4; ++x)
 #pragma unroll
                                 for (int y = 0; y < D / 32; ++y) found |= ((vw[x][y] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
                             if (__any_sync(0xFFFFFFFFu, found != 0u)) {
-                                uint32_t see[RT][4];
+                                uint32_t see[NT][2];
 #pragma unroll
-                                for (int r = 0; r < RT; ++r)
+                                for (int r = 0; r < NT; ++r)
 #pragma unroll
-                                    for (int z = 0; z < 4; ++z) {
-                                        const uint32_t b = bits[r][z & 1] >> (16 * h + 8 * (z >> 1) + 2 * t);
-                                        see[r][z] = ((b & 1u) ? 0x3C00u : 0u) | ((b & 2u) ? 0x3C000000u : 0u);
+                                    for (int z = 0; z < 2; ++z) {
+                                        const int at = 16 * h + 8 * z + g;
+                                        see[r][z] = transpose8x8((bits[r][0] >> at & 1u) * 0x3C00u | (bits[r][1] >> at & 1u) * 0x3C000000u);
                                     }
 #pragma unroll
-                                for (int y = 0; y < D / 32; ++y) {
+                                for (int w = 0; w < D / 32; ++w) {
                                     uint32_t ind[4];
 #pragma unroll
                                     for (int x = 0; x < 4; ++x) {
-                                        const uint32_t nan =
-                                            ((((vw[x][y] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu;
-                                        vw[x][y] &= ~nan;
+                                        const uint32_t nan = ((((vw[x][w] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu;
+                                        vw[x][w] &= ~nan;
                                         ind[x] = nan & 0x38383838u;  // e4m3 1.0
                                     }
-                                    const uint32_t x0 = __byte_perm(ind[0], ind[1], 0x5140), x1 = __byte_perm(ind[0], ind[1], 0x7362);
-                                    const uint32_t y0 = __byte_perm(ind[2], ind[3], 0x5140), y1 = __byte_perm(ind[2], ind[3], 0x7362);
 #pragma unroll
-                                    for (int b = 0; b < 4; ++b) {
-                                        const uint32_t ux = b < 2 ? x0 : x1, uy = b < 2 ? y0 : y1;
-                                        const uint32_t b0 = (b & 1) ? halves_of<INT8, false>(ux) : halves_of<INT8, true>(ux);
-                                        const uint32_t b1 = (b & 1) ? halves_of<INT8, false>(uy) : halves_of<INT8, true>(uy);
+                                    for (int b = 0; b < 2; ++b) {
+                                        uint32_t a[4];
+                                        columns(ind[0], ind[1], ind[2], ind[3], b, a);
 #pragma unroll
-                                        for (int r = 0; r < RT; ++r) {
+                                        for (int r = 0; r < NT; ++r) {
                                             float hit[4] = {0.f, 0.f, 0.f, 0.f};
-                                            mma16816(hit, see[r], b0, b1);
+                                            mma16816(hit, a, see[r][0], see[r][1]);
 #pragma unroll
                                             for (int z = 0; z < 4; ++z)
-                                                if (hit[z] > 0.f) o[r][4 * y + b][z] = __int_as_float(0x7FFFFFFF);
+                                                if (hit[z] > 0.f) o[r][2 * w + b][z] = __int_as_float(0x7FFFFFFF);
                                         }
                                     }
                                 }
                             }
                         }
 #pragma unroll
-                        for (int y = 0; y < D / 32; ++y) {
-                            // 4 x 4 bytes: token-major words -> for each column its four tokens
-                            const uint32_t w0 = flip<INT8>(vw[0][y]), w1 = flip<INT8>(vw[1][y]), w2 = flip<INT8>(vw[2][y]),
-                                           w3 = flip<INT8>(vw[3][y]);
-                            const uint32_t x0 = __byte_perm(w0, w1, 0x5140), x1 = __byte_perm(w0, w1, 0x7362);
-                            const uint32_t y0 = __byte_perm(w2, w3, 0x5140), y1 = __byte_perm(w2, w3, 0x7362);
+                        for (int w = 0; w < D / 32; ++w) {
+                            const uint32_t w0 = flip<INT8>(vw[0][w]), w1 = flip<INT8>(vw[1][w]), w2 = flip<INT8>(vw[2][w]),
+                                           w3 = flip<INT8>(vw[3][w]);
 #pragma unroll
-                            for (int b = 0; b < 4; ++b) {
-                                const uint32_t ux = b < 2 ? x0 : x1, uy = b < 2 ? y0 : y1;
-                                const uint32_t b0 = (b & 1) ? halves_of<INT8, false>(ux) : halves_of<INT8, true>(ux);
-                                const uint32_t b1 = (b & 1) ? halves_of<INT8, false>(uy) : halves_of<INT8, true>(uy);
+                            for (int b = 0; b < 2; ++b) {
+                                uint32_t a[4];
+                                columns(w0, w1, w2, w3, b, a);
 #pragma unroll
-                                for (int r = 0; r < RT; ++r) mma16816(o[r][4 * y + b], pa[r][h], b0, b1);
+                                for (int r = 0; r < NT; ++r) mma16816(o[r][2 * w + b], a, pb[r][h][0], pb[r][h][1]);
                             }
                         }
                     }
@@ -716,31 +777,23 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_attention_kernel(const
 
             // ---- the four warps' parts of the segment become one
             __syncthreads();
-            constexpr int kPitch = D + 4;
-            float* s_o = reinterpret_cast<float*>(smem);                       // [warp][row][kPitch]
-            float* s_m = s_o + kPagedWarps * kRows * kPitch;                   // [warp][row][4]
-            static_assert(kPagedWarps * kRows * (kPitch + 4) * 4 <= Stage::kSmem, "the parts fit the stages");
+            float* s_o = reinterpret_cast<float*>(smem);               // [warp][row][kPitch]
+            float* s_m = s_o + kPagedWarps * kRows * Stage::kPitch;    // [warp][row][4]
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
+            for (int r = 0; r < NT; ++r)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float sum = l[r][h];
-                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-                    const int row = warp * kRows + 16 * r + 8 * h + g;
-                    if (t == 0) {
-                        s_m[row * 4] = m[r][h];
-                        s_m[row * 4 + 1] = mo[r][h];
-                        s_m[row * 4 + 2] = sum;
-                    }
-                    // column c of output tile x holds d = c * (D / 8) + x
+                for (int y = 0; y < 2; ++y) {
+                    float sum = l[r][y];
+                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 4);
+                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
+                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
+                    const int row = warp * kRows + 8 * r + 2 * t + y;
+                    if (g == 0) *reinterpret_cast<float4*>(s_m + row * 4) = make_float4(m[r][y], mo[r][y], sum, 0.f);
+                    // tile x holds columns g * (D / 8) + 2 x and + 1 of V
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
-#pragma unroll
-                        for (int x = 0; x < kOut; x += 4)
-                            *reinterpret_cast<float4*>(s_o + row * kPitch + (2 * t + y) * (D / 8) + x) =
-                                make_float4(o[r][x][2 * h + y], o[r][x + 1][2 * h + y], o[r][x + 2][2 * h + y],
-                                            o[r][x + 3][2 * h + y]);
+                    for (int x = 0; x < kOut; x += 2)
+                        *reinterpret_cast<float4*>(s_o + row * Stage::kPitch + g * (D / 8) + 2 * x) =
+                            make_float4(o[r][x][y], o[r][x][2 + y], o[r][x + 1][y], o[r][x + 1][2 + y]);
                 }
             __syncthreads();
             const bool whole = t0 == 0 && t1 == tiles;
@@ -758,36 +811,37 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_attention_kernel(const
             for (int x = tid; x < kRows * (D / 4); x += kPagedThreads) {
                 const int row = x / (D / 4), d = (x % (D / 4)) * 4;
                 if (row0 + row >= rows_all) continue;
+                float4 sm[kPagedWarps];
                 float mm = -INFINITY, mmo = -INFINITY;
 #pragma unroll
                 for (int w = 0; w < kPagedWarps; ++w) {
-                    mm = fmaxf(mm, s_m[(w * kRows + row) * 4]);
-                    mmo = fmaxf(mmo, s_m[(w * kRows + row) * 4 + 1]);
+                    sm[w] = *reinterpret_cast<const float4*>(s_m + (w * kRows + row) * 4);
+                    mm = fmaxf(mm, sm[w].x);
+                    mmo = fmaxf(mmo, sm[w].y);
                 }
                 const float ref = mm == -INFINITY ? 0.f : mm, refo = mmo == -INFINITY ? 0.f : mmo;
                 float sum = 0.f;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int w = 0; w < kPagedWarps; ++w) {
-                    const float* sm = s_m + (w * kRows + row) * 4;
-                    sum += sm[2] * exp2_fast(sm[0] - ref);
-                    const float f = exp2_fast(sm[1] - refo);
-                    const float4 v = *reinterpret_cast<const float4*>(s_o + (w * kRows + row) * kPitch + d);
+                    sum += sm[w].z * exp2_fast(sm[w].x - ref);
+                    const float f = exp2_fast(sm[w].y - refo);
+                    const float4 v = *reinterpret_cast<const float4*>(s_o + (w * kRows + row) * Stage::kPitch + d);
                     acc.x = fmaf(f, v.x, acc.x);
                     acc.y = fmaf(f, v.y, acc.y);
                     acc.z = fmaf(f, v.z, acc.z);
                     acc.w = fmaf(f, v.w, acc.w);
                 }
                 if (whole) {
-                    const int64_t qi = (row0 + row) / p.group;
-                    const int hq = head * p.group + static_cast<int>(row0 + row - qi * p.group);
+                    const int up_q = static_cast<int>(static_cast<uint32_t>(in_group + row) / static_cast<uint32_t>(p.group));
+                    const int64_t token = s_seq.s.q0 + qi0 + up_q;
+                    const int hq = head * p.group + in_group + row - up_q * p.group;
                     // (a NaN sum is a row whose scores are NaN)
                     const float f = sum == 0.f ? 0.f : exp2_fast(refo - ref) / sum;
                     const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * f, acc.y * f), b = __floats2bfloat162_rn(acc.z * f, acc.w * f);
-                    *reinterpret_cast<uint2*>(p.out + ((s_seq.s.q0 + qi) * p.Hq + hq) * D + d) =
+                    *reinterpret_cast<uint2*>(p.out + (token * p.Hq + hq) * D + d) =
                         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-                    if (d == 0)
-                        p.lse[static_cast<int64_t>(hq) * p.T + s_seq.s.q0 + qi] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+                    if (d == 0) p.lse[static_cast<int64_t>(hq) * p.T + token] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
                 } else {
                     *reinterpret_cast<float4*>(p.part_o + (slot * kRows + row) * D + d) = acc;
                     if (d == 0) *reinterpret_cast<float4*>(p.part_m + (slot * kRows + row) * 4) = make_float4(mm, mmo, sum, 0.f);
@@ -797,7 +851,24 @@ __global__ void __launch_bounds__(kPagedThreads, 2) paged_attention_kernel(const
             first_segment = false;
             off += t1 - t0;
             left -= t1 - t0;
+            t0 = 0;
+            if (++head == c.heads) {
+                head = 0;
+                ++tile_row;
+            }
         }
+        // ---- the next sequence that has queries
+        off = 0;
+        if (left <= 0) break;
+        do {
+            if (++i >= p.n) return;
+            if (per_thread == 1) {
+                if (tid == i) describe(own);
+            } else if (tid == 0) {
+                describe(paged_seq(p, i));
+            }
+            __syncthreads();
+        } while (s_seq.weight == 0);
     }
 }
 

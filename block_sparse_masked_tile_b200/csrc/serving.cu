@@ -401,39 +401,44 @@ extern "C" bsmt_status bsmt_cache_compact(const bsmt_kv_cache* cache, int32_t* l
 namespace {
 
 std::mutex g_paged_mu;
-bool g_paged_set[64][16] = {{false}};
+bool g_paged_set[64][24] = {{false}};
 
 // O, the maxima and sums of two parts for each block, and the blocks' heads.
 int64_t paged_ws_bytes(int64_t D) {
     return int64_t(kMaxPartBlocks) * 2 * 32 * (D + 4) * 4 + round256(int64_t(kMaxPartBlocks) * 32);
 }
 
-template <int D, bool INT8, int RT, bool MODS>
+template <int D, bool INT8, int NT, bool MODS>
 bsmt_status launch_paged(int dev, int nsm, bsmt::PagedParams p, const bsmt::MaskDnf& dnf, cudaStream_t s) {
-    auto kern = bsmt::paged_attention_kernel<D, INT8, RT, MODS>;
-    constexpr int smem = bsmt::paged_smem<D, RT>();
+    auto kern = bsmt::paged_attention_kernel<D, INT8, NT, MODS>;
+    constexpr int smem = bsmt::PagedStage<D, NT>::kSmem;
     {
         std::lock_guard<std::mutex> lk(g_paged_mu);
-        bool& set = g_paged_set[dev][(D == 128 ? 8 : 0) + (INT8 ? 4 : 0) + (RT > 1 ? 2 : 0) + (MODS ? 1 : 0)];
+        bool& set = g_paged_set[dev][(D == 128 ? 12 : 0) + (INT8 ? 6 : 0) + (NT / 2) * 2 + (MODS ? 1 : 0)];
         if (!set) {
             const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
             if (e != cudaSuccess) return fail(BSMT_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
             set = true;
         }
     }
-    const int blocks = std::min(2 * nsm, kMaxPartBlocks);
+    const int blocks = std::min(bsmt::PagedStage<D, NT>::kBlocks * nsm, kMaxPartBlocks);
     kern<<<blocks, bsmt::kPagedThreads, smem, s>>>(p, dnf);
     TRY(launched("paged_attention"));
-    bsmt::paged_combine_kernel<D, 16 * RT><<<dim3(blocks, 16 * RT), bsmt::kPagedThreads, 0, s>>>(p);
+    bsmt::paged_combine_kernel<D, 8 * NT><<<dim3(blocks, 8 * NT), bsmt::kPagedThreads, 0, s>>>(p);
     TRY(launched("paged_attention combine"));
     return BSMT_OK;
 }
 
+template <int D, bool INT8, int NT>
+bsmt_status launch_paged_mods(bool mods, int dev, int nsm, const bsmt::PagedParams& p, const bsmt::MaskDnf& dnf, cudaStream_t s) {
+    return mods ? launch_paged<D, INT8, NT, true>(dev, nsm, p, dnf, s) : launch_paged<D, INT8, NT, false>(dev, nsm, p, dnf, s);
+}
+
 template <int D, bool INT8>
-bsmt_status launch_paged_kind(int rt, bool mods, int dev, int nsm, const bsmt::PagedParams& p, const bsmt::MaskDnf& dnf, cudaStream_t s) {
-    if (rt == 1)
-        return mods ? launch_paged<D, INT8, 1, true>(dev, nsm, p, dnf, s) : launch_paged<D, INT8, 1, false>(dev, nsm, p, dnf, s);
-    return mods ? launch_paged<D, INT8, 2, true>(dev, nsm, p, dnf, s) : launch_paged<D, INT8, 2, false>(dev, nsm, p, dnf, s);
+bsmt_status launch_paged_kind(int nt, bool mods, int dev, int nsm, const bsmt::PagedParams& p, const bsmt::MaskDnf& dnf, cudaStream_t s) {
+    if (nt == 1) return launch_paged_mods<D, INT8, 1>(mods, dev, nsm, p, dnf, s);
+    if (nt == 2) return launch_paged_mods<D, INT8, 2>(mods, dev, nsm, p, dnf, s);
+    return launch_paged_mods<D, INT8, 4>(mods, dev, nsm, p, dnf, s);
 }
 
 }  // namespace
@@ -501,15 +506,16 @@ extern "C" bsmt_status bsmt_paged_attention(const void* q, int64_t T, int64_t Hq
     p.alibi_first = sa.mode == 4;
     p.alibi_h0 = sa.alibi_h0;
     p.alibi_heads = sa.alibi_heads;
-    // Row tiles of 16, or two of them a block once an average sequence has more rows.
-    const int rt = T * p.group > 16 * std::max<int64_t>(n, 1) ? 2 : 1;
+    // Row tiles of 8, 16 or 32: the smallest that holds an average sequence's rows, so that its keys are read once.
+    const int64_t rows = (T * p.group + std::max<int64_t>(n, 1) - 1) / std::max<int64_t>(n, 1);
+    const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
     const bool mods = sa.mode != 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     bsmt_status st;
     if (p.c.dim == 128)
-        st = p.c.int8 ? launch_paged_kind<128, true>(rt, mods, dev, nsm, p, dnf, s) : launch_paged_kind<128, false>(rt, mods, dev, nsm, p, dnf, s);
+        st = p.c.int8 ? launch_paged_kind<128, true>(nt, mods, dev, nsm, p, dnf, s) : launch_paged_kind<128, false>(nt, mods, dev, nsm, p, dnf, s);
     else
-        st = p.c.int8 ? launch_paged_kind<64, true>(rt, mods, dev, nsm, p, dnf, s) : launch_paged_kind<64, false>(rt, mods, dev, nsm, p, dnf, s);
+        st = p.c.int8 ? launch_paged_kind<64, true>(nt, mods, dev, nsm, p, dnf, s) : launch_paged_kind<64, false>(nt, mods, dev, nsm, p, dnf, s);
     if (st != BSMT_OK) return st;
     return ok();
 }
