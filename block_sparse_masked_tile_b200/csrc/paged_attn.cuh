@@ -28,9 +28,9 @@
 // and P to 8 bits, and 16-bit ones from shared or tensor memory, which would cost
 // a write of every converted tile; eight rows need no such rate.
 //
-// Softmax in base 2 with two running maxima for each row: m of the scores, for
-// the sum l, and mo of score + log2(v_scale), for O, so that P * v_scale, a half,
-// never exceeds 1 whatever the pages' scales are.
+// Softmax in base 2 with two references for each row: m of the scores, for the
+// sum l, and mo of score + log2(v_scale), for O, so that P * v_scale, a half, stays
+// in range whatever the pages' scales are. They follow the running maxima lazily.
 #pragma once
 #include <cstdint>
 
@@ -46,6 +46,7 @@ namespace bsmt {
 constexpr int kPagedWarps = 4;
 constexpr int kPagedThreads = 32 * kPagedWarps;
 constexpr int kTileTokens = 32;
+constexpr float kLazy = 8.f;  // log2 by which a score may pass its reference: P stays below 2^8, far inside a half
 
 struct PagedParams {
     KvCache c;
@@ -528,11 +529,11 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
             if (kQShared) __syncthreads();
 
             float o[NT][kOut][4];
-            float m[NT][2], mo[NT][2], l[NT][2];
+            float m[NT][2], mo[NT][2], l[NT][2], shift[NT][2];  // shift: 2^(m - mo)
 #pragma unroll
             for (int r = 0; r < NT; ++r) {
 #pragma unroll
-                for (int y = 0; y < 2; ++y) m[r][y] = mo[r][y] = -INFINITY, l[r][y] = 0.f;
+                for (int y = 0; y < 2; ++y) m[r][y] = mo[r][y] = -INFINITY, l[r][y] = shift[r][y] = 0.f;
 #pragma unroll
                 for (int x = 0; x < kOut; ++x)
 #pragma unroll
@@ -636,42 +637,53 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
                                     if (!(bits[r][e & 1] >> (16 * h + 8 * (e >> 1) + g) & 1u)) s[r][h][e] = -INFINITY;
                     }
 
-                    uint32_t pb[NT][2][2];
+                    // The references stay while no score passes one by more than kLazy: then the lanes need not
+                    // agree on a maximum, and O is not rescaled.
+                    float f[NT][2][2];  // a score is s * f, f > 0 (a scale of 0 belongs to codes of 0)
+                    bool grows = false;
 #pragma unroll
-                    for (int r = 0; r < NT; ++r) {
-                        float ao[2], al[2], ref[2], f[2][2], cf[2][2];
+                    for (int r = 0; r < NT; ++r)
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            float top[2];  // of each 16 tokens
+                        for (int y = 0; y < 2; ++y)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                // a score is s * f, f > 0 (a scale of 0 belongs to codes of 0)
-                                f[y][h] = MODS ? 1.f : fmaxf(qs[r][y] * ks[h], 1e-37f);
-                                top[h] = fmaxf(s[r][h][y], s[r][h][2 + y]);
-                                top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], 4));
-                                top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], 8));
-                                top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], 16));
-                                if (!MODS) top[h] *= f[y][h];
+                                f[r][y][h] = MODS ? 1.f : fmaxf(qs[r][y] * ks[h], 1e-37f);
+                                const float top = fmaxf(s[r][h][y], s[r][h][2 + y]) * f[r][y][h];
+                                grows = grows || top > m[r][y] + kLazy || top + ev[h] > mo[r][y] + kLazy;
                             }
-                            const float mn = fmaxf(m[r][y], fmaxf(top[0], top[1]));
-                            const float mon = fmaxf(mo[r][y], fmaxf(top[0] + ev[0], top[1] + ev[1]));
-                            ref[y] = mn == -INFINITY ? 0.f : mn;
-                            const float refo = mon == -INFINITY ? 0.f : mon;
-                            al[y] = exp2_fast(m[r][y] - ref[y]);
-                            ao[y] = exp2_fast(mo[r][y] - refo);
-                            const float shift = mn == -INFINITY ? 0.f : exp2_fast(ref[y] - refo);
-                            cf[y][0] = vs[0] * shift;
-                            cf[y][1] = vs[1] * shift;
-                            m[r][y] = mn;
-                            mo[r][y] = mon;
-                        }
-                        if (__any_sync(0xFFFFFFFFu, ao[0] != 1.f || ao[1] != 1.f)) {
+                    if (__any_sync(0xFFFFFFFFu, grows)) {
+#pragma unroll
+                        for (int r = 0; r < NT; ++r) {
+                            float ao[2];
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                float top[2];  // of each 16 tokens
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    top[h] = fmaxf(s[r][h][y], s[r][h][2 + y]) * f[r][y][h];
+                                    top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], 4));
+                                    top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], 8));
+                                    top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], 16));
+                                }
+                                const float mn = fmaxf(m[r][y], fmaxf(top[0], top[1]));
+                                const float mon = fmaxf(mo[r][y], fmaxf(top[0] + ev[0], top[1] + ev[1]));
+                                const float ref = mn == -INFINITY ? 0.f : mn, refo = mon == -INFINITY ? 0.f : mon;
+                                l[r][y] *= exp2_fast(m[r][y] - ref);
+                                ao[y] = exp2_fast(mo[r][y] - refo);
+                                shift[r][y] = mn == -INFINITY ? 0.f : exp2_fast(ref - refo);
+                                m[r][y] = mn;
+                                mo[r][y] = mon;
+                            }
 #pragma unroll
                             for (int x = 0; x < kOut; ++x)
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) o[r][x][e] *= ao[e & 1];
                         }
-                        float sum[2] = {0.f, 0.f};
+                    }
+                    uint32_t pb[NT][2][2];
+#pragma unroll
+                    for (int r = 0; r < NT; ++r) {
+                        const float ref[2] = {m[r][0] == -INFINITY ? 0.f : m[r][0], m[r][1] == -INFINITY ? 0.f : m[r][1]};
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -679,14 +691,12 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
                                 float e[2];
 #pragma unroll
                                 for (int y = 0; y < 2; ++y) {
-                                    e[y] = exp2_fast(MODS ? s[r][h][2 * z + y] - ref[y] : fmaf(s[r][h][2 * z + y], f[y][h], -ref[y]));
-                                    sum[y] += e[y];
+                                    e[y] = exp2_fast(MODS ? s[r][h][2 * z + y] - ref[y] : fmaf(s[r][h][2 * z + y], f[r][y][h], -ref[y]));
+                                    l[r][y] += e[y];
                                 }
                                 // P to 11 bits: an error of 2^-12 of each term, below the output's bf16 rounding
-                                pb[r][h][z] = transpose8x8(pack_half2(e[0] * cf[0][h], e[1] * cf[1][h]));
+                                pb[r][h][z] = transpose8x8(pack_half2(e[0] * (vs[h] * shift[r][0]), e[1] * (vs[h] * shift[r][1])));
                             }
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) l[r][y] = l[r][y] * al[y] + sum[y];
                     }
 
 #pragma unroll
