@@ -1507,4 +1507,19 @@ bsmt_status status_word(int dev, int** addr) {
     return BSMT_OK;
 }
 
+bsmt_status encode_rows(CUtensorMap* map, void* base, int64_t rows, int row_bytes, int box) {
+    EncodeTiledFn enc = nullptr;
+    const bsmt_status st = get_encoder(&enc);
+    if (st != BSMT_OK) return st;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+    const cuuint32_t boxes[2] = {static_cast<cuuint32_t>(row_bytes), static_cast<cuuint32_t>(box)};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return ::fail(BSMT_ERR_CUDA, "cuTensorMapEncodeTiled (rows) failed (%d)", static_cast<int>(r));
+    return BSMT_OK;
+}
+
 }  // namespace bsmt_host

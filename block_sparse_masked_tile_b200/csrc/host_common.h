@@ -4,6 +4,8 @@
 #pragma once
 #include <cstdint>
 
+#include <cuda.h>
+
 #include "bsmt.h"
 #include "mask_dnf.cuh"
 
@@ -34,5 +36,9 @@ bsmt_status score_args(const bsmt_score_spec* score, int64_t Hq, ScoreArgs* out)
 bsmt_status sm_count(int* dev, int* n);
 // Device address of the current device's status word.
 bsmt_status status_word(int dev, int** addr);
+
+// Tensor map of `rows` rows of `row_bytes` (64 or 128) bytes, copied `box` rows at a
+// time with the swizzle of their length. `base` 16-byte aligned.
+bsmt_status encode_rows(CUtensorMap* map, void* base, int64_t rows, int row_bytes, int box);
 
 }  // namespace bsmt_host

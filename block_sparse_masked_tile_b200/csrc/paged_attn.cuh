@@ -11,12 +11,12 @@
 // in the workspace, which paged_combine_kernel joins in a fixed order.
 //
 // Bound by HBM: K and V codes are read once. Each warp of a block takes every
-// fourth tile of the share and has its own pipeline of cp.async stages. Which
-// bytes of a tile a lane copies is chosen so that it is the lane that uses them:
-// the contraction's order is free, so a lane's 16 bytes of a K row are the four
-// k positions of four MMA steps, and its 16 bytes of a V row are one row of each
-// of 16 half output tiles. No barrier, shared-memory transpose or bank conflict
-// comes in.
+// fourth tile of the share and has its own ring of slots, which TMA fills: one copy
+// of 4 KB for the K and one for the V of a tile (two of 2 KB with pages of 16), all
+// four warps of three blocks an SM keeping some 150 KB loaded or on their way. The
+// contraction's order is free, so a lane's 16 bytes of a K row are the four k
+// positions of four MMA steps, and its 16 bytes of a V row are one row of each of 16
+// half output tiles: wide shared loads, no transposes, no barrier between warps.
 //
 // The products are S^T = K q^T and O^T = V^T P^T: tokens and then columns of V are
 // the 16 rows of mma.sync m16n8k16, the query rows its 8 columns. A decoded token
@@ -34,6 +34,7 @@
 #pragma once
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -67,36 +68,58 @@ struct PagedParams {
 };
 
 // Up to 32 registers of O a thread (NT * D <= 128): three blocks an SM with 16 KB of
-// stages a warp; more: two blocks, 24 KB a warp.
+// slots a warp; more: two blocks, 24 KB a warp. A slot holds the K or the V codes of a tile.
 template <int D, int NT>
-struct PagedStage {
+struct PagedShape {
     static constexpr int kBlocks = NT * D > 128 ? 2 : 3;  // of an SM
-    static constexpr int kK = kTileTokens * D, kV = kTileTokens * D;
-    static constexpr int kBytes = kK + kV + 16;  // and the page scales: k, k, v, v
-    static constexpr int kStages = (kBlocks == 2 ? 3 : 2) * (128 / D);
-    static constexpr int kWarpBytes = kStages * kBytes;
-    static constexpr int kPitch = D + 4;  // floats of a row where the warps' parts meet
-    static constexpr int kMerge = kPagedWarps * 8 * NT * (kPitch + 4) * 4;
-    static constexpr int kQ = kPagedWarps * kWarpBytes > kMerge ? kPagedWarps * kWarpBytes : kMerge;
-    static constexpr int kSmem = kQ + (NT > 2 ? NT * (D / 16) * 256 : 0);  // NT = 4: q's fragments, too
+    static constexpr int kSlot = kTileTokens * D;
+    static constexpr int kDeep = (kBlocks == 2 ? 3 : 2) * (128 / D);  // tiles a warp has loaded or on their way
+    static constexpr int kWarpBytes = 2 * kDeep * kSlot;
+    static constexpr int kPitch = D + 4;  // floats of a row where the warps' parts meet (in the slots)
+    static_assert(kPagedWarps * 8 * NT * (kPitch + 4) * 4 <= kPagedWarps * kWarpBytes, "the parts fit the slots");
+    static constexpr int kQ = kPagedWarps * kWarpBytes;
+    static constexpr int kSmem = kQ + (NT > 2 ? NT * (D / 16) * 256 : 0) + 1024;  // NT = 4: q's fragments; alignment
 };
 
 __device__ __forceinline__ uint32_t shared_addr(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool there) {
-    const uint32_t n = there ? BYTES : 0;  // 0: the destination is zeroed and src not read
-    if (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(BYTES) : "memory");
+// Rows [row, row + box) of a pool into a slot; the slot's barrier counts the bytes.
+__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(bar)
+        : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void bar_init(uint32_t bar) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Waits for a slot. A load that does not come within 2 s is reported
+// (BSMT_ERR_DEVICE_TIMEOUT) and the kernel goes on to its end.
+__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, int* status) {
+    if (bar_try(bar, parity)) return;
+    uint64_t t0, now;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    while (!bar_try(bar, parity)) {
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        if (now - t0 > 2000000000ull) {
+            set_status(status, BSMT_ERR_DEVICE_TIMEOUT);
+            return;
+        }
+    }
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -109,12 +132,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
     return r;
 }
-__device__ __forceinline__ float4 lds128f(uint32_t a) {
-    float4 r;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "r"(a));
-    return r;
-}
-
 __device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
@@ -241,7 +258,7 @@ struct PagedSeqShared {
     int64_t weight;  // tiles of all its units
     int tiles, row_tiles, runs;
     int first[kMaxTerms], last[kMaxTerms];          // runs of seen tiles
-    int64_t clean_lo[kMaxTerms], clean_hi[kMaxTerms];  // keys that every query sees, for each term
+    int32_t clean_lo[kMaxTerms], clean_hi[kMaxTerms];  // keys that every query sees, for each term
 };
 
 // A sequence without a key still has one (empty) tile, which writes its rows.
@@ -252,9 +269,10 @@ __device__ __forceinline__ int64_t paged_weight(const PagedParams& p, const Page
 }
 
 template <int D, bool INT8, int NT, bool MODS>
-__global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
-    paged_attention_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ MaskDnf dnf) {
-    using Stage = PagedStage<D, NT>;
+__global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
+    paged_attention_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ MaskDnf dnf,
+                           const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+    using Shape = PagedShape<D, NT>;
     constexpr int kSteps = D / 16;   // MMA steps over the head dimension
     constexpr int kChunks = D / 64;  // 16-byte pieces of a K row that one lane holds
     constexpr int kOut = D / 16;     // output tiles of 16 columns of V
@@ -262,7 +280,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
     constexpr bool kQShared = NT > 2;  // q's fragments in shared memory, not registers
     constexpr float kLog2e = 1.4426950408889634f;
     constexpr float kLn2 = 0.6931471805599453f;
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t s_bars[kPagedWarps * 2 * Shape::kDeep];
     __shared__ long long s_scan[kPagedWarps];
     __shared__ long long s_off;
     __shared__ int s_i;
@@ -270,6 +289,10 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
     const KvCache& c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
+    uint8_t* const smem = smem_raw + (1024u - (shared_addr(smem_raw) & 1023u)) % 1024u;  // (the swizzle's period)
+    const uint32_t bars = shared_addr(s_bars) + warp * 2 * Shape::kDeep * 8;
+    if (lane < 2 * Shape::kDeep) bar_init(bars + lane * 8);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 
     // ---- this block's share of all tiles
     const int per_thread = (p.n + kPagedThreads - 1) / kPagedThreads;
@@ -279,9 +302,11 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
         s_seq.tiles = seen_tiles(dnf, s.len - s.count, s.len - 1, s.len, s_seq.first, s_seq.last, &s_seq.runs);
         s_seq.weight = paged_weight(p, s, s_seq.tiles, kRows);
         for (int x = 0; x < dnf.n_terms; ++x) {
-            int64_t unused;
-            term_interval(dnf, x, s.len - 1, 0, s.len - 1, 0, 0, s_seq.clean_lo[x], unused);
-            term_interval(dnf, x, s.len - s.count, 0, s.len - 1, 0, 0, unused, s_seq.clean_hi[x]);
+            int64_t lo, hi, unused;  // (both within [-len, len])
+            term_interval(dnf, x, s.len - 1, 0, s.len - 1, 0, 0, lo, unused);
+            term_interval(dnf, x, s.len - s.count, 0, s.len - 1, 0, 0, unused, hi);
+            s_seq.clean_lo[x] = static_cast<int32_t>(min(lo, static_cast<int64_t>(INT32_MAX)));
+            s_seq.clean_hi[x] = static_cast<int32_t>(max(hi, static_cast<int64_t>(-1)));
         }
     };
     long long mine = 0;
@@ -349,17 +374,31 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
     int i = s_i;
     long long off = s_off, left = end - begin;
     bool first_segment = true;
-    const uint32_t stages = shared_addr(smem) + warp * Stage::kWarpBytes;
-    const uint32_t lane_stage = stages + lane * 16, lane_v = stages + Stage::kK + lane * (D / 8);
-    const int64_t head_bytes = static_cast<int64_t>(c.page) * D;
-    const int64_t page_bytes = head_bytes * c.heads;
-    const uint8_t* const k_pool = c.k + static_cast<int64_t>(p.layer) * c.pages * page_bytes + g * D + 16 * t;
-    const uint8_t* const v_pool = c.v + static_cast<int64_t>(p.layer) * c.pages * page_bytes + 2 * t * D + g * (D / 8);
-    const float* const k_scales = c.k_scale + static_cast<int64_t>(p.layer) * c.pages * c.heads;
-    const float* const v_scales = c.v_scale + static_cast<int64_t>(p.layer) * c.pages * c.heads;
+    const uint32_t slots = shared_addr(smem) + warp * Shape::kWarpBytes;  // K of tile x, V of tile x, ...
+    const float* const lane_scales = ((lane & 2) ? c.v_scale : c.k_scale) + static_cast<int64_t>(p.layer) * c.pages * c.heads;
+    // The slots hold rows of D bytes whose 16-byte pieces the copy has swizzled: piece ^ row % 8 (D = 128), piece ^
+    // row / 2 % 4 (D = 64). Token `slot_token(g)` of each 8 is the products' row g: the order in which neither the K
+    // reads (rows g, pieces t) nor the V reads (rows 2 t and 2 t + 1, pieces g) meet a bank twice.
+    auto slot_token = [](int x) {
+        const int u = x >> 1;
+        if (D == 128) return (x & 1) ? ((2 * u) ^ 4) | 1 : 2 * u;
+        const int even = (u & 1) | (u >> 1) << 2;
+        return (x & 1) ? even ^ 3 : even;
+    };
+    const int tok_g = slot_token(g);
+    uint32_t k_at[kChunks], v_at[2];  // this lane's pieces of the first 8 rows
+#pragma unroll
+    for (int x = 0; x < kChunks; ++x) k_at[x] = tok_g * D + (D == 128 ? ((4 * x + t) ^ tok_g) * 16 : (t ^ (tok_g >> 1)) * 16);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int row = slot_token(2 * t + x);
+        v_at[x] = row * D + (D == 128 ? (g ^ row) * 16 : ((g >> 1) ^ (row >> 1)) * 16 + (g & 1) * 8);
+    }
+    uint32_t bar_k = bars, parity = 0;  // the next tile's barriers (K, then V) and their phase
+    uint32_t slot_k = slots;
 
     while (true) {
-        const int64_t len = s_seq.s.len;
+        const int len = static_cast<int>(s_seq.s.len);
         const int count = s_seq.s.count;
         const int seen = s_seq.tiles, tiles = max(seen, 1);
         const int64_t weight = s_seq.weight;
@@ -382,88 +421,65 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
             const int in_group = static_cast<int>(row0 - qi0 * p.group);  // row0 = qi0 * group + in_group
 
             // ---- pipeline over this warp's tiles
-            const uint8_t* const k_head = k_pool + head * head_bytes;
-            const uint8_t* const v_head = v_pool + head * head_bytes;
             int run = 0, run_base = 0;  // the run that the next tile to load lies in, and the tiles before it
-            auto tile_of = [&](int ord) -> int64_t {  // first token of the unit's tile `ord`; -1: none
+            auto tile_of = [&](int ord) -> int {  // first token of the unit's tile `ord`; -1: none
                 if (ord >= t1 || ord >= seen) return -1;
                 while (ord - run_base > s_seq.last[run] - s_seq.first[run]) {
                     run_base += s_seq.last[run] - s_seq.first[run] + 1;
                     ++run;
                 }
-                return static_cast<int64_t>(s_seq.first[run] + ord - run_base) * kTileTokens;
+                return (s_seq.first[run] + ord - run_base) * kTileTokens;
             };
-            auto page_at = [&](int64_t tok) -> int {  // page of a token; -1: behind the sequence
+            auto page_at = [&](int tok) -> int {  // page of a token; -1: behind the sequence
                 if (tok < 0 || tok >= len) return -1;
                 return __ldg(table + (tok >> c.page_shift));
             };
             int next_ord = t0 + warp;
-            int64_t next_tok = tile_of(next_ord);
+            int next_tok = tile_of(next_ord);
             int next_a = page_at(next_tok), next_b = page_at(next_tok < 0 ? -1 : next_tok + 16);
-            auto issue = [&](int stage) {
-                const uint32_t st = stage * Stage::kBytes;
-                if (next_tok >= 0) {
-                    int pa = next_a, pb = next_b;
-                    const bool ok_a = pa >= 0 && pa < c.pages, ok_b = pb >= 0 && pb < c.pages;
-                    const int in_a = static_cast<int>(next_tok) & (c.page - 1), in_b = (static_cast<int>(next_tok) + 16) & (c.page - 1);
-                    if (!ok_a) pa = 0;
-                    if (!ok_b) pb = 0;
-                    const int64_t base_a = pa * page_bytes + in_a * D, base_b = pb * page_bytes + in_b * D;
-                    if (ok_a && ok_b && next_tok + kTileTokens <= len) {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-#pragma unroll
-                            for (int x = 0; x < kChunks; ++x)
-                                cp_async<16>(lane_stage + st + (j * kChunks + x) * 512,
-                                             k_head + (j < 2 ? base_a : base_b) + (j & 1) * 8 * D + 64 * x, true);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                cp_async<D / 8>(lane_v + st + (h * 4 + x) * 32 * (D / 8),
-                                                v_head + (h ? base_b : base_a) + ((x & 1) + 8 * (x >> 1)) * D, true);
-                    } else {
-                        // the sequence's last tile, or a bad page: rows that are not there are zeros
-                        const int have = static_cast<int>(min(static_cast<int64_t>(kTileTokens), len - next_tok));
-                        if ((!ok_a || (!ok_b && have > 16)) && lane == 0) set_status(p.status, BSMT_ERR_DEVICE_BOUNDS);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-#pragma unroll
-                            for (int x = 0; x < kChunks; ++x)
-                                cp_async<16>(lane_stage + st + (j * kChunks + x) * 512,
-                                             k_head + (j < 2 ? base_a : base_b) + (j & 1) * 8 * D + 64 * x,
-                                             8 * j + g < have && (j < 2 ? ok_a : ok_b));
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                cp_async<D / 8>(lane_v + st + (h * 4 + x) * 32 * (D / 8),
-                                                v_head + (h ? base_b : base_a) + ((x & 1) + 8 * (x >> 1)) * D,
-                                                16 * h + 2 * t + (x & 1) + 8 * (x >> 1) < have && (h ? ok_b : ok_a));
-                    }
-                    if (lane < 4) {
-                        const float* src = ((lane & 2) ? v_scales : k_scales) + static_cast<int64_t>((lane & 1) ? pb : pa) * c.heads + head;
-                        cp_async<4>(stages + st + Stage::kK + Stage::kV + lane * 4, src, (lane & 1) ? ok_b : ok_a);
-                    }
+            int tok_q[Shape::kDeep];      // first tokens of the tiles on their way
+            int row_a[Shape::kDeep], row_b[Shape::kDeep];  // their rows in the pools
+            float scale_q[Shape::kDeep];  // lane % 4: k_scale of the tile's halves of 16 tokens, v_scale of them
+            const int no_row = c.layers * c.pages * c.heads * c.page;  // behind the pool: a load gives zeros
+            auto load = [&](const CUtensorMap* map, uint32_t slot, uint32_t bar, int ra, int rb) {
+                if (lane == 0) {
+                    bar_expect(bar, Shape::kSlot);
+                    load_rows(slot, map, ra, bar);
+                    if (c.page == 16) load_rows(slot + 16 * D, map, rb, bar);
                 }
-                cp_async_commit();
+            };
+            // Finds the rows of the next tile and starts its K load; its V load follows once that slot is free.
+            auto begin_tile = [&](int x, uint32_t slot, uint32_t bar) {
+                tok_q[x] = next_tok;
+                if (next_tok >= 0) {
+                    const bool ok_a = next_a >= 0 && next_a < c.pages, ok_b = next_b >= 0 && next_b < c.pages;
+                    if ((!ok_a || (!ok_b && next_tok + 16 < len)) && lane == 0) set_status(p.status, BSMT_ERR_DEVICE_BOUNDS);
+                    row_a[x] = ok_a ? ((p.layer * c.pages + next_a) * c.heads + head) * c.page + (next_tok & (c.page - 1)) : no_row;
+                    row_b[x] = ok_b ? ((p.layer * c.pages + next_b) * c.heads + head) * c.page + ((next_tok + 16) & (c.page - 1)) : no_row;
+                    scale_q[x] = ((lane & 1) ? ok_b : ok_a) ? __ldg(lane_scales + static_cast<int64_t>((lane & 1) ? next_b : next_a) * c.heads + head) : 0.f;
+                    load(&k_map, slot, bar, row_a[x], row_b[x]);
+                }
                 next_ord += kPagedWarps;
                 next_tok = tile_of(next_ord);
                 next_a = page_at(next_tok);
                 next_b = page_at(next_tok < 0 ? -1 : next_tok + 16);
             };
-            int64_t tok_q[Stage::kStages];  // first tokens of the tiles in flight
+            {
+                uint32_t slot = slot_k, bar = bar_k;
 #pragma unroll
-            for (int x = 0; x < Stage::kStages; ++x) {
-                tok_q[x] = next_tok;
-                issue(x);
+                for (int x = 0; x < Shape::kDeep; ++x) {
+                    begin_tile(x, slot, bar);
+                    if (tok_q[x] >= 0) load(&v_map, slot + Shape::kSlot, bar + 8, row_a[x], row_b[x]);
+                    slot = slot + 2 * Shape::kSlot == slots + Shape::kWarpBytes ? slots : slot + 2 * Shape::kSlot;
+                    bar = bar + 16 == bars + 16 * Shape::kDeep ? bars : bar + 16;
+                }
             }
 
             // ---- q: row g of each 8, in halves; what the softmax needs of rows 2 t and 2 t + 1
             uint32_t qf[kQShared ? 1 : NT][kSteps][2];
             float qs[NT][2], slope[NT][2];
-            int64_t pos[NT][2];
-            const uint32_t q_smem = shared_addr(smem) + Stage::kQ + lane * 8;
+            int pos[NT][2];
+            const uint32_t q_smem = shared_addr(smem) + Shape::kQ + lane * 8;
 #pragma unroll
             for (int r = 0; r < NT; ++r) {
                 const int row = 8 * r + g;
@@ -516,7 +532,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
                     const int col = 8 * r + 2 * t + y;
                     const int up_c = static_cast<int>(static_cast<uint32_t>(in_group + col) / static_cast<uint32_t>(p.group));
                     qs[r][y] = __shfl_sync(0xFFFFFFFFu, row_scale, (2 * t + y) * 4);
-                    pos[r][y] = len - count + qi0 + up_c;
+                    pos[r][y] = len - count + static_cast<int>(qi0) + up_c;
                     slope[r][y] = 0.f;
                     if (MODS && p.alibi && row0 + col < rows_all) {
                         const int h = head * p.group + in_group + col - up_c * p.group;
@@ -540,14 +556,10 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
                     for (int y = 0; y < 4; ++y) o[r][x][y] = 0.f;
             }
 
-            int stage = 0;
             for (int ord = t0 + warp; ord < t1; ord += kPagedWarps) {
-                cp_async_wait<Stage::kStages - 1>();
-                __syncwarp();
-                const int64_t tok = tok_q[0];
-                const uint32_t st = stage * Stage::kBytes;
+                const int tok = tok_q[0];
                 if (tok >= 0) {
-                    // s[r][h][2 z + y]: token 16 h + 8 z + g, row 8 r + 2 t + y
+                    // s[r][h][2 z + y]: token 16 h + 8 z + tok_g, row 8 r + 2 t + y
                     float s[NT][2][4];
 #pragma unroll
                     for (int r = 0; r < NT; ++r)
@@ -555,12 +567,13 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
                         for (int h = 0; h < 2; ++h)
 #pragma unroll
                             for (int y = 0; y < 4; ++y) s[r][h][y] = 0.f;
+                    bar_wait(bar_k, parity, p.status);
 #pragma unroll
                     for (int x = 0; x < kChunks; ++x) {
                         uint32_t kw[4][4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const uint4 v = lds128(lane_stage + st + (j * kChunks + x) * 512);
+                            const uint4 v = lds128(slot_k + k_at[x] + j * 8 * D);
                             kw[j][0] = flip<INT8>(v.x), kw[j][1] = flip<INT8>(v.y), kw[j][2] = flip<INT8>(v.z), kw[j][3] = flip<INT8>(v.w);
                         }
 #pragma unroll
@@ -585,9 +598,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
                             }
                         }
                     }
-                    const uint32_t sc = stages + st + Stage::kK + Stage::kV;
-                    const float4 scales = lds128f(sc);
-                    const float ks[2] = {scales.x, scales.y}, vs[2] = {scales.z, scales.w};
+                    const float ks[2] = {__shfl_sync(0xFFFFFFFFu, scale_q[0], 0), __shfl_sync(0xFFFFFFFFu, scale_q[0], 1)};
+                    const float vs[2] = {__shfl_sync(0xFFFFFFFFu, scale_q[0], 2), __shfl_sync(0xFFFFFFFFu, scale_q[0], 3)};
                     const float ev[2] = {__log2f(fmaxf(vs[0], 0x1p-126f)), __log2f(fmaxf(vs[1], 0x1p-126f))};
 
                     // which keys the rows see
@@ -609,7 +621,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
                             }
                     }
                     if (MODS) {
-                        const int rel = static_cast<int>(tok - pos[0][0]) + g;
+                        const int rel = tok - pos[0][0] + tok_g;
 #pragma unroll
                         for (int r = 0; r < NT; ++r)
 #pragma unroll
@@ -619,7 +631,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
                                     const int y = e & 1;
                                     float z = s[r][h][e] * (qs[r][y] * ks[h]);
                                     const float bias = slope[r][y] * static_cast<float>(rel + 16 * h + 8 * (e >> 1) -
-                                                                                        static_cast<int>(pos[r][y] - pos[0][0]));
+                                                                                        (pos[r][y] - pos[0][0]));
                                     if (p.alibi_first) z += bias;
                                     // cap * tanh(z / cap), tanh(u) = 1 - 2 / (exp(2 u) + 1)
                                     if (p.softcap) z = p.cap * (1.f - __fdividef(2.f, exp2_fast(z * (2.f * kLog2e / p.cap)) + 1.f));
@@ -634,7 +646,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
                             for (int h = 0; h < 2; ++h)
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
-                                    if (!(bits[r][e & 1] >> (16 * h + 8 * (e >> 1) + g) & 1u)) s[r][h][e] = -INFINITY;
+                                    if (!(bits[r][e & 1] >> (16 * h + 8 * (e >> 1) + tok_g) & 1u)) s[r][h][e] = -INFINITY;
                     }
 
                     // The references stay while no score passes one by more than kLazy: then the lanes need not
@@ -680,6 +692,15 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
                                 for (int e = 0; e < 4; ++e) o[r][x][e] *= ao[e & 1];
                         }
                     }
+                    // every lane has used the K slot (the vote above needed its scores): the tile kDeep further goes there
+#pragma unroll
+                    for (int x = 0; x + 1 < Shape::kDeep; ++x) {
+                        tok_q[x] = tok_q[x + 1];
+                        row_a[x] = row_a[x + 1];
+                        row_b[x] = row_b[x + 1];
+                        scale_q[x] = scale_q[x + 1];
+                    }
+                    begin_tile(Shape::kDeep - 1, slot_k, bar_k);
                     uint32_t pb[NT][2][2];
 #pragma unroll
                     for (int r = 0; r < NT; ++r) {
@@ -699,12 +720,13 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
                             }
                     }
 
+                    bar_wait(bar_k + 8, parity, p.status);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {  // 16 tokens
                         uint32_t vw[4][D / 32];
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            const uint32_t a = lane_v + st + (h * 4 + x) * 32 * (D / 8);
+                            const uint32_t a = slot_k + Shape::kSlot + v_at[x & 1] + (16 * h + 8 * (x >> 1)) * D;
                             if (D == 128) {
                                 const uint4 v = lds128(a);
                                 vw[x][0] = v.x, vw[x][1] = v.y, vw[x][D / 32 - 2] = v.z, vw[x][D / 32 - 1] = v.w;
@@ -734,7 +756,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
                                 for (int r = 0; r < NT; ++r)
 #pragma unroll
                                     for (int z = 0; z < 2; ++z) {
-                                        const int at = 16 * h + 8 * z + g;
+                                        const int at = 16 * h + 8 * z + tok_g;
                                         see[r][z] = transpose8x8((bits[r][0] >> at & 1u) * 0x3C00u | (bits[r][1] >> at & 1u) * 0x3C000000u);
                                     }
 #pragma unroll
@@ -776,19 +798,24 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
                         }
                     }
                 }
-                __syncwarp();  // every lane has read the stage's scales
-#pragma unroll
-                for (int x = 0; x + 1 < Stage::kStages; ++x) tok_q[x] = tok_q[x + 1];
-                tok_q[Stage::kStages - 1] = next_tok;
-                issue(stage);
-                stage = stage + 1 == Stage::kStages ? 0 : stage + 1;
+                if (tok >= 0) {
+                    __syncwarp();  // every lane has read the V slot
+                    if (tok_q[Shape::kDeep - 1] >= 0)
+                        load(&v_map, slot_k + Shape::kSlot, bar_k + 8, row_a[Shape::kDeep - 1], row_b[Shape::kDeep - 1]);
+                    slot_k += 2 * Shape::kSlot;
+                    bar_k += 16;
+                    if (slot_k == slots + Shape::kWarpBytes) {
+                        slot_k = slots;
+                        bar_k = bars;
+                        parity ^= 1;
+                    }
+                }
             }
-            cp_async_wait<0>();
 
             // ---- the four warps' parts of the segment become one
             __syncthreads();
             float* s_o = reinterpret_cast<float*>(smem);               // [warp][row][kPitch]
-            float* s_m = s_o + kPagedWarps * kRows * Stage::kPitch;    // [warp][row][4]
+            float* s_m = s_o + kPagedWarps * kRows * Shape::kPitch;    // [warp][row][4]
 #pragma unroll
             for (int r = 0; r < NT; ++r)
 #pragma unroll
@@ -802,7 +829,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
                     // tile x holds columns g * (D / 8) + 2 x and + 1 of V
 #pragma unroll
                     for (int x = 0; x < kOut; x += 2)
-                        *reinterpret_cast<float4*>(s_o + row * Stage::kPitch + g * (D / 8) + 2 * x) =
+                        *reinterpret_cast<float4*>(s_o + row * Shape::kPitch + g * (D / 8) + 2 * x) =
                             make_float4(o[r][x][y], o[r][x][2 + y], o[r][x + 1][y], o[r][x + 1][2 + y]);
                 }
             __syncthreads();
@@ -836,7 +863,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
                 for (int w = 0; w < kPagedWarps; ++w) {
                     sum += sm[w].z * exp2_fast(sm[w].x - ref);
                     const float f = exp2_fast(sm[w].y - refo);
-                    const float4 v = *reinterpret_cast<const float4*>(s_o + (w * kRows + row) * Stage::kPitch + d);
+                    const float4 v = *reinterpret_cast<const float4*>(s_o + (w * kRows + row) * Shape::kPitch + d);
                     acc.x = fmaf(f, v.x, acc.x);
                     acc.y = fmaf(f, v.y, acc.y);
                     acc.z = fmaf(f, v.z, acc.z);
@@ -857,6 +884,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedStage<D, NT>::kBlocks)
                     if (d == 0) *reinterpret_cast<float4*>(p.part_m + (slot * kRows + row) * 4) = make_float4(mm, mmo, sum, 0.f);
                 }
             }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the slots take copies again
             __syncthreads();
             first_segment = false;
             off += t1 - t0;

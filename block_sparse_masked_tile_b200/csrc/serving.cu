@@ -411,7 +411,7 @@ int64_t paged_ws_bytes(int64_t D) {
 template <int D, bool INT8, int NT, bool MODS>
 bsmt_status launch_paged(int dev, int nsm, bsmt::PagedParams p, const bsmt::MaskDnf& dnf, cudaStream_t s) {
     auto kern = bsmt::paged_attention_kernel<D, INT8, NT, MODS>;
-    constexpr int smem = bsmt::PagedStage<D, NT>::kSmem;
+    constexpr int smem = bsmt::PagedShape<D, NT>::kSmem;
     {
         std::lock_guard<std::mutex> lk(g_paged_mu);
         bool& set = g_paged_set[dev][(D == 128 ? 12 : 0) + (INT8 ? 6 : 0) + (NT / 2) * 2 + (MODS ? 1 : 0)];
@@ -421,8 +421,13 @@ bsmt_status launch_paged(int dev, int nsm, bsmt::PagedParams p, const bsmt::Mask
             set = true;
         }
     }
-    const int blocks = std::min(bsmt::PagedStage<D, NT>::kBlocks * nsm, kMaxPartBlocks);
-    kern<<<blocks, bsmt::kPagedThreads, smem, s>>>(p, dnf);
+    const int blocks = std::min(bsmt::PagedShape<D, NT>::kBlocks * nsm, kMaxPartBlocks);
+    // the pools as rows of D codes; a copy takes the rows of a tile that lie in one page
+    const int64_t rows = int64_t(p.c.layers) * p.c.pages * p.c.heads * p.c.page;
+    CUtensorMap k_map, v_map;
+    TRY(encode_rows(&k_map, p.c.k, rows, D, std::min(p.c.page, bsmt::kTileTokens)));
+    TRY(encode_rows(&v_map, p.c.v, rows, D, std::min(p.c.page, bsmt::kTileTokens)));
+    kern<<<blocks, bsmt::kPagedThreads, smem, s>>>(p, dnf, k_map, v_map);
     TRY(launched("paged_attention"));
     bsmt::paged_combine_kernel<D, 8 * NT><<<dim3(blocks, 8 * NT), bsmt::kPagedThreads, 0, s>>>(p);
     TRY(launched("paged_attention combine"));
@@ -479,6 +484,9 @@ extern "C" bsmt_status bsmt_paged_attention(const void* q, int64_t T, int64_t Hq
     TRY(build_dnf(mask_spec, 1, &dnf));
     ScoreArgs sa;
     TRY(score_args(score, Hq, &sa));
+    if (int64_t(p.c.layers) * p.c.pages * p.c.heads * p.c.page > kMaxLen)
+        return fail(BSMT_ERR_UNSUPPORTED, "paged attention: a pool of %d layers, %d pages and %d heads has more than %lld rows",
+                    p.c.layers, p.c.pages, p.c.heads, static_cast<long long>(kMaxLen));
     if (T == 0) return ok();
     TRY(check_workspace(workspace, workspace_bytes, paged_ws_bytes(p.c.dim)));
     int dev = 0, nsm = 0;
