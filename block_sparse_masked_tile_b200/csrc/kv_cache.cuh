@@ -28,6 +28,12 @@ struct KvCache {
     int32_t layers, pages, heads, page, page_shift, dim, max_seqs, max_pages, int8;
 };
 
+// N elements that are loaded or stored at once.
+template <typename E, int N>
+struct alignas(sizeof(E) * N) Pack {
+    E v[N];
+};
+
 constexpr int kMinScaleExp = -120;  // a page of zeros has this scale
 
 __device__ __forceinline__ void set_status(int* status, int code) { atomicCAS(status, 0, code); }

@@ -68,7 +68,8 @@ struct PagedParams {
 };
 
 // Up to 32 registers of O a thread (NT * D <= 128): three blocks an SM with 16 KB of
-// slots a warp; more: two blocks, 24 KB a warp. A slot holds the K or the V codes of a tile.
+// slots a warp; more: two blocks, 24 KB a warp (three, with spills, took 1.4 times as
+// long at NT = 2). A slot holds the K or the V codes of a tile.
 template <int D, int NT>
 struct PagedShape {
     static constexpr int kBlocks = NT * D > 128 ? 2 : 3;  // of an SM
@@ -76,9 +77,9 @@ struct PagedShape {
     static constexpr int kDeep = (kBlocks == 2 ? 3 : 2) * (128 / D);  // tiles a warp has loaded or on their way
     static constexpr int kWarpBytes = 2 * kDeep * kSlot;
     static constexpr int kPitch = D + 4;  // floats of a row where the warps' parts meet (in the slots)
-    static_assert(kPagedWarps * 8 * NT * (kPitch + 4) * 4 <= kPagedWarps * kWarpBytes, "the parts fit the slots");
+    static_assert(8 * NT * (kPitch + 4) * 4 <= kWarpBytes, "a warp's part fits its slots");
     static constexpr int kQ = kPagedWarps * kWarpBytes;
-    static constexpr int kSmem = kQ + (NT > 2 ? NT * (D / 16) * 256 : 0) + 1024;  // NT = 4: q's fragments; alignment
+    static constexpr int kSmem = kQ + (NT > 1 ? NT * (D / 16) * 256 : 0) + 1024;  // NT > 1: q's fragments; alignment
 };
 
 __device__ __forceinline__ uint32_t shared_addr(const void* p) {
@@ -182,7 +183,7 @@ __device__ __forceinline__ uint32_t flip(uint32_t w) {
 
 // The tiles that some query in [q_lo, q_hi] of a sequence of `len` tokens sees:
 // up to kMaxTerms disjoint runs, ascending. Returns the number of tiles.
-__device__ __forceinline__ int seen_tiles(const MaskDnf& dnf, int64_t q_lo, int64_t q_hi, int64_t len, int* first,
+__device__ __noinline__ int seen_tiles(const MaskDnf& dnf, int64_t q_lo, int64_t q_hi, int64_t len, int* first,
                                           int* last, int* runs) {
     int n = 0, total = 0;
     for (int t = 0; t < dnf.n_terms; ++t) {
@@ -224,7 +225,7 @@ struct PagedSeq {
     int count;          // queries
 };
 
-__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int i) {
+__device__ __noinline__ PagedSeq paged_seq(const PagedParams& p, int i) {
     PagedSeq s;
     s.slot = __ldg(p.seqs + i);
     int64_t q0 = i, q1 = i + 1;
@@ -261,11 +262,14 @@ struct PagedSeqShared {
     int32_t clean_lo[kMaxTerms], clean_hi[kMaxTerms];  // keys that every query sees, for each term
 };
 
-// A sequence without a key still has one (empty) tile, which writes its rows.
-__device__ __forceinline__ int64_t paged_weight(const PagedParams& p, const PagedSeq& s, int tiles, int rows_of_tile) {
+// A unit weighs its tiles and what it costs to begin and end one, in tiles. A
+// sequence without a key still has one (empty) tile, which writes its rows.
+constexpr int kUnitCost = 10;  // (0, 6, 12: ragged batch of 64 sequences up to 16k 215, 201, 200 us)
+template <int ROWS>
+__device__ __forceinline__ int64_t paged_weight(const PagedParams& p, const PagedSeq& s, int tiles) {
     if (s.count == 0) return 0;
-    const int64_t row_tiles = (static_cast<int64_t>(s.count) * p.group + rows_of_tile - 1) / rows_of_tile;
-    return row_tiles * p.c.heads * max(tiles, 1);
+    const int64_t row_tiles = (static_cast<int64_t>(s.count) * p.group + ROWS - 1) / ROWS;
+    return row_tiles * p.c.heads * (max(tiles, 1) + kUnitCost);
 }
 
 template <int D, bool INT8, int NT, bool MODS>
@@ -277,7 +281,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
     constexpr int kChunks = D / 64;  // 16-byte pieces of a K row that one lane holds
     constexpr int kOut = D / 16;     // output tiles of 16 columns of V
     constexpr int kRows = 8 * NT;
-    constexpr bool kQShared = NT > 2;  // q's fragments in shared memory, not registers
+    constexpr bool kQShared = NT > 1;  // q's fragments in shared memory, not registers
     constexpr float kLog2e = 1.4426950408889634f;
     constexpr float kLn2 = 0.6931471805599453f;
     extern __shared__ uint8_t smem_raw[];
@@ -289,6 +293,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
     const KvCache& c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
+    asm volatile("griddepcontrol.launch_dependents;");  // the combining kernel may take its place, and waits for this one's end
     uint8_t* const smem = smem_raw + (1024u - (shared_addr(smem_raw) & 1023u)) % 1024u;  // (the swizzle's period)
     const uint32_t bars = shared_addr(s_bars) + warp * 2 * Shape::kDeep * 8;
     if (lane < 2 * Shape::kDeep) bar_init(bars + lane * 8);
@@ -300,7 +305,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
     auto describe = [&](const PagedSeq& s) {  // what the whole block needs of a sequence
         s_seq.s = s;
         s_seq.tiles = seen_tiles(dnf, s.len - s.count, s.len - 1, s.len, s_seq.first, s_seq.last, &s_seq.runs);
-        s_seq.weight = paged_weight(p, s, s_seq.tiles, kRows);
+        s_seq.weight = paged_weight<kRows>(p, s, s_seq.tiles);
         for (int x = 0; x < dnf.n_terms; ++x) {
             int64_t lo, hi, unused;  // (both within [-len, len])
             term_interval(dnf, x, s.len - 1, 0, s.len - 1, 0, 0, lo, unused);
@@ -316,7 +321,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
         own = paged_seq(p, i);
         int first[kMaxTerms], last[kMaxTerms], runs;
         const int tiles = seen_tiles(dnf, own.len - own.count, own.len - 1, own.len, first, last, &runs);
-        mine += paged_weight(p, own, tiles, kRows);
+        mine += paged_weight<kRows>(p, own, tiles);
     }
     long long incl = mine;
 #pragma unroll
@@ -345,7 +350,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
                 own = paged_seq(p, i);
                 int first[kMaxTerms], last[kMaxTerms], runs;
                 const int tiles = seen_tiles(dnf, own.len - own.count, own.len - 1, own.len, first, last, &runs);
-                const long long w = paged_weight(p, own, tiles, kRows);
+                const long long w = paged_weight<kRows>(p, own, tiles);
                 if (off < w) break;
                 off -= w;
             }
@@ -404,18 +409,23 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
         const int64_t weight = s_seq.weight;
         const int32_t* table = c.page_table + static_cast<int64_t>(max(s_seq.s.slot, 0)) * c.max_pages;
         const int64_t rows_all = static_cast<int64_t>(count) * p.group;
-        int64_t unit = 0;
-        int t0 = 0;
+        int unit = 0, in_unit = 0;  // in_unit: of the unit's weight, its cost first
         if (off != 0) {
-            unit = off / tiles;
-            t0 = static_cast<int>(off - unit * tiles);
+            const long long u = off <= 0x7FFFFFFF ? static_cast<uint32_t>(off) / static_cast<uint32_t>(tiles + kUnitCost) : off / (tiles + kUnitCost);
+            unit = static_cast<int>(u);
+            in_unit = static_cast<int>(off - u * (tiles + kUnitCost));
         }
-        int64_t tile_row = unit / c.heads;
-        int head = static_cast<int>(unit - tile_row * c.heads);
+        int tile_row = unit / c.heads;
+        int head = unit - tile_row * c.heads;
 
         while (off < weight && left > 0) {
-            const int t1 = static_cast<int>(min(static_cast<long long>(tiles), t0 + left));
-            const int64_t row0 = tile_row * kRows;  // the unit's first row
+            const int take = static_cast<int>(min(static_cast<long long>(tiles + kUnitCost - in_unit), left));
+            const int t0 = max(0, in_unit - kUnitCost), t1 = max(0, in_unit + take - kUnitCost);
+            off += take;
+            left -= take;
+            in_unit = 0;
+            if (t1 == 0) break;  // (the share ends before the unit's first tile)
+            const int64_t row0 = static_cast<int64_t>(tile_row) * kRows;  // the unit's first row
             const int64_t qi0 = rows_all < 0x7FFFFFFF ? static_cast<int64_t>(static_cast<uint32_t>(row0) / static_cast<uint32_t>(p.group))
                                                       : row0 / p.group;
             const int in_group = static_cast<int>(row0 - qi0 * p.group);  // row0 = qi0 * group + in_group
@@ -434,9 +444,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
                 if (tok < 0 || tok >= len) return -1;
                 return __ldg(table + (tok >> c.page_shift));
             };
-            int next_ord = t0 + warp;
-            int next_tok = tile_of(next_ord);
-            int next_a = page_at(next_tok), next_b = page_at(next_tok < 0 ? -1 : next_tok + 16);
+            int next_ord = t0 + warp;  // (after the first loads: the tile that find_next has found)
+            int next_tok = -1, next_a = -1, next_b = -1;
             int tok_q[Shape::kDeep];      // first tokens of the tiles on their way
             int row_a[Shape::kDeep], row_b[Shape::kDeep];  // their rows in the pools
             float scale_q[Shape::kDeep];  // lane % 4: k_scale of the tile's halves of 16 tokens, v_scale of them
@@ -459,20 +468,33 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
                     scale_q[x] = ((lane & 1) ? ok_b : ok_a) ? __ldg(lane_scales + static_cast<int64_t>((lane & 1) ? next_b : next_a) * c.heads + head) : 0.f;
                     load(&k_map, slot, bar, row_a[x], row_b[x]);
                 }
-                next_ord += kPagedWarps;
-                next_tok = tile_of(next_ord);
-                next_a = page_at(next_tok);
-                next_b = page_at(next_tok < 0 ? -1 : next_tok + 16);
+            };
+            auto find_next = [&](int tok, int a, int b) {
+                next_tok = tok;
+                next_a = a;
+                next_b = b;
             };
             {
+                int first_tok[Shape::kDeep + 1], first_a[Shape::kDeep + 1], first_b[Shape::kDeep + 1];  // (read together)
+#pragma unroll
+                for (int x = 0; x <= Shape::kDeep; ++x) {
+                    first_tok[x] = tile_of(next_ord + x * kPagedWarps);
+                    first_a[x] = page_at(first_tok[x]);
+                    first_b[x] = page_at(first_tok[x] < 0 ? -1 : first_tok[x] + 16);
+                }
                 uint32_t slot = slot_k, bar = bar_k;
 #pragma unroll
                 for (int x = 0; x < Shape::kDeep; ++x) {
+                    next_tok = first_tok[x];
+                    next_a = first_a[x];
+                    next_b = first_b[x];
                     begin_tile(x, slot, bar);
                     if (tok_q[x] >= 0) load(&v_map, slot + Shape::kSlot, bar + 8, row_a[x], row_b[x]);
                     slot = slot + 2 * Shape::kSlot == slots + Shape::kWarpBytes ? slots : slot + 2 * Shape::kSlot;
                     bar = bar + 16 == bars + 16 * Shape::kDeep ? bars : bar + 16;
                 }
+                find_next(first_tok[Shape::kDeep], first_a[Shape::kDeep], first_b[Shape::kDeep]);
+                next_ord += Shape::kDeep * kPagedWarps;
             }
 
             // ---- q: row g of each 8, in halves; what the softmax needs of rows 2 t and 2 t + 1
@@ -701,6 +723,9 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
                         scale_q[x] = scale_q[x + 1];
                     }
                     begin_tile(Shape::kDeep - 1, slot_k, bar_k);
+                    next_ord += kPagedWarps;
+                    const int found = tile_of(next_ord);
+                    find_next(found, page_at(found), page_at(found < 0 ? -1 : found + 16));
                     uint32_t pb[NT][2][2];
 #pragma unroll
                     for (int r = 0; r < NT; ++r) {
@@ -887,9 +912,6 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the slots take copies again
             __syncthreads();
             first_segment = false;
-            off += t1 - t0;
-            left -= t1 - t0;
-            t0 = 0;
             if (++head == c.heads) {
                 head = 0;
                 ++tile_row;
@@ -911,67 +933,84 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
 }
 
 // Joins the parts of the units that share boundaries cut: a unit that begins in
-// block b ends in block b + parts - 1, and its later parts are those blocks'
-// first. One block for each (block b, row); its warps take every fourth part.
+// block b's share ends in that of block b + parts - 1, and its later parts are those
+// blocks' first. A block has four rows: a warp for each, or, with many parts, all
+// warps on one row after another, each taking every fourth part.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kPagedThreads) paged_combine_kernel(const __grid_constant__ PagedParams p) {
     constexpr float kLn2 = 0.6931471805599453f;
     constexpr int kPer = D / 32;  // columns of one lane
+    constexpr int kFew = 16;
     __shared__ float s_o[kPagedWarps][D];
-    const int32_t* hd = p.heads_of_parts + blockIdx.x * 8;
-    const int parts = hd[0];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4* hd = reinterpret_cast<const int4*>(p.heads_of_parts + blockIdx.x * 8);
+    const int4 h0 = hd[0];
+    const int parts = h0.x;
     if (parts == 0) return;
-    const int64_t row0 = static_cast<int64_t>(static_cast<uint32_t>(hd[5])) | static_cast<int64_t>(hd[6]) << 32;
-    const int64_t row = row0 + blockIdx.y;
-    if (row >= static_cast<int64_t>(hd[3]) * p.group) return;
+    const int4 h1 = hd[1];
+    const int64_t row0 = static_cast<int64_t>(static_cast<uint32_t>(h1.y)) | static_cast<int64_t>(h1.z) << 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    auto slot_of = [&](int j) -> int64_t {
-        return (2 * (static_cast<int64_t>(blockIdx.x) + j) + (j == 0 ? hd[1] : 0)) * ROWS + blockIdx.y;
-    };
-    float m = -INFINITY, mo = -INFINITY;
-    for (int j = lane; j < parts; j += 32) {
-        const float4 v = *reinterpret_cast<const float4*>(p.part_m + slot_of(j) * 4);
-        m = fmaxf(m, v.x);
-        mo = fmaxf(mo, v.y);
+    const bool few = parts <= kFew;
+    for (int x = few ? warp : 0; x < kPagedWarps; x += few ? kPagedWarps : 1) {
+        const int in_tile = blockIdx.y * kPagedWarps + x;
+        const int64_t row = row0 + in_tile;
+        if (row >= static_cast<int64_t>(h0.w) * p.group) return;  // (uniform over the warps that share a row)
+        auto slot_of = [&](int j) -> int64_t {
+            return (2 * (static_cast<int64_t>(blockIdx.x) + j) + (j == 0 ? h0.y : 0)) * ROWS + in_tile;
+        };
+        float m = -INFINITY, mo = -INFINITY;
+        for (int j = lane; j < parts; j += 32) {
+            const float4 v = *reinterpret_cast<const float4*>(p.part_m + slot_of(j) * 4);
+            m = fmaxf(m, v.x);
+            mo = fmaxf(mo, v.y);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+            mo = fmaxf(mo, __shfl_xor_sync(0xFFFFFFFFu, mo, d));
+        }
+        const float ref = m == -INFINITY ? 0.f : m, refo = mo == -INFINITY ? 0.f : mo;
+        float sum = 0.f;
+        for (int j = lane; j < parts; j += 32) {
+            const float4 v = *reinterpret_cast<const float4*>(p.part_m + slot_of(j) * 4);
+            sum += v.z * exp2_fast(v.x - ref);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+        float acc[kPer];
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) acc[y] = 0.f;
+#pragma unroll 8
+        for (int j = few ? 0 : warp; j < parts; j += few ? 1 : kPagedWarps) {
+            const int64_t s = slot_of(j);
+            const float f = exp2_fast(p.part_m[s * 4 + 1] - refo);
+            const Pack<float, kPer> v = *reinterpret_cast<const Pack<float, kPer>*>(p.part_o + s * D + lane * kPer);
+#pragma unroll
+            for (int y = 0; y < kPer; ++y) acc[y] = fmaf(f, v.v[y], acc[y]);
+        }
+        const int64_t qi = row / p.group;
+        const int hq = h1.x * p.group + static_cast<int>(row - qi * p.group);
+        const int64_t token = h0.z + qi;
+        if (!few) {
+            __syncthreads();
+#pragma unroll
+            for (int y = 0; y < kPer; ++y) s_o[warp][lane * kPer + y] = acc[y];
+            __syncthreads();
+#pragma unroll
+            for (int y = 0; y < kPer; ++y) {
+                acc[y] = 0.f;
+#pragma unroll
+                for (int w = 0; w < kPagedWarps; ++w) acc[y] += s_o[w][lane * kPer + y];
+            }
+            if (warp != 0) continue;
+        }
+        const float f = sum == 0.f ? 0.f : exp2_fast(refo - ref) / sum;
+        Pack<__nv_bfloat16, kPer> r;
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) r.v[y] = __float2bfloat16_rn(acc[y] * f);
+        *reinterpret_cast<Pack<__nv_bfloat16, kPer>*>(p.out + (token * p.Hq + hq) * D + lane * kPer) = r;
+        if (lane == 0) p.lse[static_cast<int64_t>(hq) * p.T + token] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-        mo = fmaxf(mo, __shfl_xor_sync(0xFFFFFFFFu, mo, d));
-    }
-    const float ref = m == -INFINITY ? 0.f : m, refo = mo == -INFINITY ? 0.f : mo;
-    float sum = 0.f;
-    for (int j = lane; j < parts; j += 32) {
-        const float4 v = *reinterpret_cast<const float4*>(p.part_m + slot_of(j) * 4);
-        sum += v.z * exp2_fast(v.x - ref);
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    float acc[kPer];
-#pragma unroll
-    for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
-#pragma unroll 4
-    for (int j = warp; j < parts; j += kPagedWarps) {
-        const int64_t s = slot_of(j);
-        const float f = exp2_fast(p.part_m[s * 4 + 1] - refo);
-        const float* src = p.part_o + s * D + lane * kPer;
-#pragma unroll
-        for (int x = 0; x < kPer; ++x) acc[x] = fmaf(f, src[x], acc[x]);
-    }
-#pragma unroll
-    for (int x = 0; x < kPer; ++x) s_o[warp][lane * kPer + x] = acc[x];
-    __syncthreads();
-    const int64_t qi = row / p.group;
-    const int hq = hd[4] * p.group + static_cast<int>(row - qi * p.group);
-    const int64_t token = hd[2] + qi;
-    const float f = sum == 0.f ? 0.f : exp2_fast(refo - ref) / sum;
-    for (int d = threadIdx.x; d < D; d += kPagedThreads) {
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < kPagedWarps; ++w) v += s_o[w][d];
-        p.out[(token * p.Hq + hq) * D + d] = __float2bfloat16_rn(v * f);
-    }
-    if (threadIdx.x == 0) p.lse[static_cast<int64_t>(hq) * p.T + token] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
 }
 
 }  // namespace bsmt

@@ -22,6 +22,7 @@
 #include <cuda_runtime.h>
 
 #include "bsmt_serving.h"
+#include "kv_cache.cuh"
 
 namespace bsmt {
 
@@ -42,11 +43,6 @@ struct RotaryParams {
     int64_t pos_axis, pos_b, pos_t;
     int64_t tokens;  // B * T
     int32_t T, head_dim, pairs, heads, chunk, inverse;
-};
-
-template <typename E, int N>
-struct alignas(sizeof(E) * N) Pack {
-    E v[N];
 };
 
 __device__ __forceinline__ float to_f32(float x) { return x; }

@@ -429,7 +429,18 @@ bsmt_status launch_paged(int dev, int nsm, bsmt::PagedParams p, const bsmt::Mask
     TRY(encode_rows(&v_map, p.c.v, rows, D, std::min(p.c.page, bsmt::kTileTokens)));
     kern<<<blocks, bsmt::kPagedThreads, smem, s>>>(p, dnf, k_map, v_map);
     TRY(launched("paged_attention"));
-    bsmt::paged_combine_kernel<D, 8 * NT><<<dim3(blocks, 8 * NT), bsmt::kPagedThreads, 0, s>>>(p);
+    // The combining kernel is set up while the first one runs, and waits for its end on the device.
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks, 2 * NT);
+    cfg.blockDim = dim3(bsmt::kPagedThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, bsmt::paged_combine_kernel<D, 8 * NT>, p);
+    if (e != cudaSuccess) return fail(BSMT_ERR_CUDA, "paged_attention combine launch: %s", cudaGetErrorString(e));
     TRY(launched("paged_attention combine"));
     return BSMT_OK;
 }
@@ -505,7 +516,7 @@ extern "C" bsmt_status bsmt_paged_attention(const void* q, int64_t T, int64_t Hq
     p.layer = layer;
     p.Hq = static_cast<int32_t>(Hq);
     p.group = static_cast<int32_t>(Hq / p.c.heads);
-    p.min_share = 8;  // two tiles for each warp of a block
+    p.min_share = bsmt::kUnitCost + 8;  // a unit's begin and two tiles for each warp of a block
     p.scale = scale;
     p.cap = sa.cap;
     // the modes of the score program: none, soft-cap, ALiBi, soft-cap then ALiBi, ALiBi then soft-cap
