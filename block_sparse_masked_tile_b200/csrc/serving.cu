@@ -516,7 +516,7 @@ extern "C" bsmt_status bsmt_paged_attention(const void* q, int64_t T, int64_t Hq
     p.layer = layer;
     p.Hq = static_cast<int32_t>(Hq);
     p.group = static_cast<int32_t>(Hq / p.c.heads);
-    p.min_share = bsmt::kUnitCost + 8;  // a unit's begin and two tiles for each warp of a block
+    p.min_share = 8;  // two tiles for each warp of a block
     p.scale = scale;
     p.cap = sa.cap;
     // the modes of the score program: none, soft-cap, ALiBi, soft-cap then ALiBi, ALiBi then soft-cap

@@ -24,7 +24,7 @@ from typing import Iterable, Sequence
 
 import torch
 
-from . import MaskMod, ScoreMod, _check, _check_launch, _lib, _MaskSpec, _score_spec, _ScoreSpec, _stream_ptr
+from . import MaskMod, ScoreMod, _check, _check_launch, _DEBUG_SYNC, _lib, _MaskSpec, _score_spec, _ScoreSpec
 
 __all__ = [
     "RotarySpec", "rotary_spec", "rotary", "rotary_backward", "PagedCache", "create_paged_cache", "cache_extend",
@@ -37,6 +37,7 @@ _CACHE_DTYPES = {torch.float8_e4m3fn: 0, torch.int8: 1}
 _ROTARY_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 
 _i32, _i64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
+_I64x2, _I64x3 = _i64 * 2, _i64 * 3
 
 
 class _RotarySpecC(ctypes.Structure):
@@ -45,7 +46,7 @@ class _RotarySpecC(ctypes.Structure):
 
 
 class _RotaryTensor(ctypes.Structure):
-    _fields_ = [("inp", _vp), ("out", _vp), ("in_strides", _i64 * 3), ("out_strides", _i64 * 3), ("heads", _i32)]
+    _fields_ = [("inp", _vp), ("out", _vp), ("in_strides", _I64x3), ("out_strides", _I64x3), ("heads", _i32)]
 
 
 class _KvCache(ctypes.Structure):
@@ -77,6 +78,23 @@ def _declare() -> None:
 
 _declare()
 
+# Serving calls are small and many, so their way to the library is short: the
+# current device and stream as plain integers, no device switch where none is needed.
+_device_now = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_byref = ctypes.byref
+
+
+def _call(device: torch.device, f, *args) -> None:
+    """f(*args, current stream of the device), with the device current."""
+    index = device.index
+    if index == _device_now():
+        status = f(*args, torch._C._cuda_getCurrentRawStream(index))
+        if status or _DEBUG_SYNC:
+            _check_launch(status)
+    else:
+        with torch.cuda.device(device):
+            _check_launch(f(*args, torch._C._cuda_getCurrentRawStream(index)))
+
 
 # ------------------------------------------------------------------ rotary
 @dataclass(frozen=True)
@@ -99,15 +117,10 @@ class RotarySpec:
             raise ValueError(f"{pairs} rotary pairs in a head of {self.head_dim} (1 to {MAX_ROTARY_PAIRS} pairs)")
         if len(self.axis) != pairs:
             raise ValueError(f"{len(self.axis)} axes for {pairs} pairs")
-        if not 1 <= self.num_axes <= 127 or any(not 0 <= a < self.num_axes for a in self.axis):
+        if not 1 <= self.num_axes <= 127 or min(self.axis) < 0 or max(self.axis) >= self.num_axes:
             raise ValueError(f"axis values must lie in [0, {self.num_axes}), with 1 to 127 axes")
-        c = _RotarySpecC()
-        c.head_dim, c.num_pairs, c.num_axes = int(self.head_dim), pairs, int(self.num_axes)
-        c.interleaved = int(bool(self.interleaved))
-        for i in range(pairs):
-            c.inv_freq[i] = float(self.inv_freq[i])
-            c.axis[i] = int(self.axis[i])
-        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_c", _RotarySpecC(self.head_dim, pairs, self.num_axes, bool(self.interleaved),
+                                                    tuple(self.inv_freq), tuple(self.axis)))
 
 
 def rotary_spec(head_dim: int, sections: Sequence[int] | None = None, base: float = 10000.0,
@@ -121,12 +134,10 @@ def rotary_spec(head_dim: int, sections: Sequence[int] | None = None, base: floa
     sections = [int(head_dim) // 2] if sections is None else [int(s) for s in sections]
     if any(s < 0 for s in sections) or sum(sections) < 1:
         raise ValueError(f"sections {sections}: pair counts must not be negative, and some pair must turn")
-    pairs = sum(sections)
-    axis, freq = [], []
-    for a, s in enumerate(sections):
-        for j in range(s):
-            freq.append(float(base) ** (-j / s) if per_axis else float(base) ** (-len(axis) / pairs))
-            axis.append(a)
+    base = float(base)
+    axis = [a for a, s in enumerate(sections) for _ in range(s)]
+    ladders = [s for s in sections if s] if per_axis else [len(axis)]
+    freq = [base ** (-j / n) for n in ladders for j in range(n)]
     return RotarySpec(int(head_dim), tuple(freq), tuple(axis), len(sections), bool(interleaved))
 
 
@@ -141,20 +152,14 @@ def _rotary(tensors, positions: torch.Tensor, spec: RotarySpec, inverse: bool) -
     first = tensors[0]
     dev = first.device
     B, _, T, _ = _heads_tokens(first)
-    c = (_RotaryTensor * len(tensors))()
-    outs = []
-    for i, x in enumerate(tensors):
-        b, h, n, s = _heads_tokens(x)
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
-        c[i].inp, c[i].out, c[i].heads = x.data_ptr(), y.data_ptr(), h
-        c[i].in_strides[:] = s
-        c[i].out_strides[:] = _heads_tokens(y)[3]
-        outs.append(y)
-    strides = [positions.stride(0) if positions.dim() > 1 else 0,
-               positions.stride(1) if positions.dim() == 3 else 0, positions.stride(-1)]
-    with torch.cuda.device(dev):
-        _check_launch(_lib.bsmt_rotary(ctypes.byref(spec._c), _ROTARY_DTYPES[first.dtype], B, T, positions.data_ptr(),
-                                       (_i64 * 3)(*strides), int(inverse), c, len(tensors), _stream_ptr(dev)))
+    outs = [torch.empty(x.shape, dtype=x.dtype, device=dev) for x in tensors]
+    c = (_RotaryTensor * len(tensors))(*[
+        (x.data_ptr(), y.data_ptr(), _heads_tokens(x)[3], _heads_tokens(y)[3], x.shape[1]) for x, y in zip(tensors, outs)])
+    dims = positions.dim()
+    strides = _I64x3(positions.stride(0) if dims > 1 else 0, positions.stride(1) if dims == 3 else 0,
+                     positions.stride(dims - 1))
+    _call(dev, _lib.bsmt_rotary, _byref(spec._c), _ROTARY_DTYPES[first.dtype], B, T, positions.data_ptr(), strides,
+          int(inverse), c, len(tensors))
     return outs
 
 
@@ -183,7 +188,7 @@ class _RotaryFn(torch.autograd.Function):
 
 def _rotary_args(q, k, positions, spec) -> list:
     tensors = [q] if k is None else [q, k]
-    for name, t in zip(("q", "k"), tensors):
+    for name, t in zip("qk", tensors):
         if t.dtype not in _ROTARY_DTYPES:
             raise ValueError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
         if t.dim() not in (3, 4):
@@ -194,15 +199,17 @@ def _rotary_args(q, k, positions, spec) -> list:
             raise ValueError(f"{name}'s innermost dimension must be contiguous")
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
-    if k is not None and (k.dtype != q.dtype or k.device != q.device or k.dim() != q.dim()
-                          or _heads_tokens(k)[0] != _heads_tokens(q)[0] or _heads_tokens(k)[2] != _heads_tokens(q)[2]):
-        raise ValueError(f"q and k must share type, device, batch and tokens: q {tuple(q.shape)}, k {tuple(k.shape)}")
+    B, _, T, _ = _heads_tokens(q)
+    if k is not None:
+        Bk, _, Tk, _ = _heads_tokens(k)
+        if k.dtype != q.dtype or k.device != q.device or k.dim() != q.dim() or Bk != B or Tk != T:
+            raise ValueError(f"q and k must share type, device, batch and tokens: q {tuple(q.shape)}, k {tuple(k.shape)}")
     if positions.dtype != torch.int32 or positions.device != q.device:
         raise ValueError(f"positions must be int32 on {q.device} (got {positions.dtype} on {positions.device})")
-    B, _, T, _ = _heads_tokens(q)
-    shapes = [(spec.num_axes, T)] + [(T,)] * (spec.num_axes == 1) + [(spec.num_axes, B, T)] * (q.dim() == 4)
-    if tuple(positions.shape) not in shapes:
-        raise ValueError(f"positions {tuple(positions.shape)}: expected one of {shapes}")
+    shape, axes = tuple(positions.shape), spec.num_axes
+    if shape != (axes, T) and not (shape == (T,) and axes == 1) and not (shape == (axes, B, T) and q.dim() == 4):
+        raise ValueError(f"positions {shape}: expected [{axes}, {T}]" + (f", [{T}]" if axes == 1 else "")
+                         + (f" or [{axes}, {B}, {T}]" if q.dim() == 4 else ""))
     return tensors
 
 
@@ -229,14 +236,15 @@ def rotary_backward(dq: torch.Tensor, dk: torch.Tensor | None, positions: torch.
 
 
 # ------------------------------------------------------------------- cache
-@dataclass
+@dataclass(frozen=True)
 class PagedCache:
     """Keys and values of many sequences in 8-bit pages (bsmt_kv_cache).
 
     k, v: float8_e4m3fn or int8 codes [layers, pages, Hkv, page_size, D];
     k_scale, v_scale: fp32 [layers, pages, Hkv]; page_table: int32
     [max_seqs, max_pages]; seq_lens: int32 [max_seqs]; ref_counts: int32
-    [pages]. ``create_paged_cache`` makes an empty one."""
+    [pages]. ``create_paged_cache`` makes an empty one. The tensors' contents
+    change under the calls below, their places must not."""
     k: torch.Tensor
     v: torch.Tensor
     k_scale: torch.Tensor
@@ -246,24 +254,25 @@ class PagedCache:
     ref_counts: torch.Tensor
 
     def __post_init__(self):
-        if self.k.dim() != 5 or self.k.dtype not in _CACHE_DTYPES:
+        k, v, table, dev = self.k, self.v, self.page_table, self.k.device
+        if k.dim() != 5 or k.dtype not in _CACHE_DTYPES:
             raise ValueError("cache codes must be float8_e4m3fn or int8 [layers, pages, Hkv, page_size, D]")
-        layers, pages, heads, size, dim = self.k.shape
-        if self.page_table.dim() != 2:
+        if table.dim() != 2:
             raise ValueError("page_table must be [max_seqs, max_pages]")
-        seqs = self.page_table.shape[0]
-        for name, t, dtype, shape in (("v", self.v, self.k.dtype, self.k.shape),
-                                      ("k_scale", self.k_scale, torch.float32, (layers, pages, heads)),
-                                      ("v_scale", self.v_scale, torch.float32, (layers, pages, heads)),
-                                      ("page_table", self.page_table, torch.int32, self.page_table.shape),
-                                      ("seq_lens", self.seq_lens, torch.int32, (seqs,)),
-                                      ("ref_counts", self.ref_counts, torch.int32, (pages,))):
-            if t.dtype != dtype or t.shape != torch.Size(shape) or t.device != self.k.device:
-                raise ValueError(f"cache {name} must be {dtype} {tuple(shape)} on {self.k.device} "
+        layers, pages, heads, size, dim = shape = k.shape
+        seqs, wide = table.shape
+        f32, i32 = torch.float32, torch.int32
+        for name, t, dtype, want in (("k", k, k.dtype, shape), ("v", v, k.dtype, shape),
+                                     ("k_scale", self.k_scale, f32, shape[:3]), ("v_scale", self.v_scale, f32, shape[:3]),
+                                     ("page_table", table, i32, table.shape), ("seq_lens", self.seq_lens, i32, (seqs,)),
+                                     ("ref_counts", self.ref_counts, i32, (pages,))):
+            if t.dtype != dtype or t.shape != want or t.device != dev or not t.is_contiguous():
+                raise ValueError(f"cache {name} must be contiguous {dtype} {tuple(want)} on {dev} "
                                  f"(got {t.dtype} {tuple(t.shape)} on {t.device})")
-        for name in ("k", "v", "k_scale", "v_scale", "page_table", "seq_lens", "ref_counts"):
-            if not getattr(self, name).is_contiguous():
-                raise ValueError(f"cache {name} must be contiguous")
+        object.__setattr__(self, "_c", _KvCache(
+            k.data_ptr(), v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(), table.data_ptr(),
+            self.seq_lens.data_ptr(), self.ref_counts.data_ptr(), layers, pages, heads, size, dim, seqs, wide,
+            _CACHE_DTYPES[k.dtype]))
 
     @property
     def device(self) -> torch.device:
@@ -273,14 +282,12 @@ class PagedCache:
     def page_size(self) -> int:
         return self.k.shape[3]
 
-    def _struct(self) -> _KvCache:
-        if not self.k.is_cuda:
-            raise ValueError("the cache must be on a CUDA device")
-        layers, pages, heads, size, dim = self.k.shape
-        return _KvCache(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
-                        self.page_table.data_ptr(), self.seq_lens.data_ptr(), self.ref_counts.data_ptr(), layers,
-                        pages, heads, size, dim, self.page_table.shape[0], self.page_table.shape[1],
-                        _CACHE_DTYPES[self.k.dtype])
+
+def _on_gpu(cache: PagedCache) -> tuple:
+    """The cache's C form and its device."""
+    if not cache.k.is_cuda:
+        raise ValueError("the cache must be on a CUDA device")
+    return _byref(cache._c), cache.k.device
 
 
 def create_paged_cache(num_pages: int, num_kv_heads: int, head_dim: int, max_seqs: int, max_pages: int,
@@ -299,14 +306,14 @@ def create_paged_cache(num_pages: int, num_kv_heads: int, head_dim: int, max_seq
                       torch.zeros(num_pages, dtype=torch.int32, device=device))
 
 
-def _list(cache: PagedCache, name: str, t: torch.Tensor | None, n: int | None = None) -> int | None:
-    """Address of a list of int32 on the cache's device."""
+def _list(device: torch.device, name: str, t: torch.Tensor | None, n: int | None = None) -> int | None:
+    """Address of a list of n int32 on the cache's device."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.device != cache.device:
-        raise ValueError(f"{name} must be a contiguous 1-D int32 tensor on {cache.device}")
-    if n is not None and t.numel() != n:
-        raise ValueError(f"{name} has {t.numel()} entries, expected {n}")
+    if t.dtype != torch.int32 or t.dim() != 1 or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 1-D int32 tensor on {device}")
+    if n is not None and t.shape[0] != n:
+        raise ValueError(f"{name} has {t.shape[0]} entries, expected {n}")
     return t.data_ptr()
 
 
@@ -321,10 +328,9 @@ def _workspace(workspace: torch.Tensor | None, need: int, device: torch.device) 
 def cache_workspace_bytes(cache: PagedCache, n: int = 0) -> int:
     """Bytes of device workspace that cache_extend and cache_fork of n entries,
     and cache_compact (n = 0), need."""
-    c, b = _KvCache(), _i64(0)
-    c.num_pages = cache.k.shape[1]
-    _check(_lib.bsmt_cache_workspace_bytes(ctypes.byref(c), int(n), ctypes.byref(b)))
-    return int(b.value)
+    b = _i64(0)
+    _check(_lib.bsmt_cache_workspace_bytes(_byref(cache._c), int(n), _byref(b)))
+    return b.value
 
 
 def cache_extend(cache: PagedCache, seqs: torch.Tensor, counts: torch.Tensor | None = None,
@@ -333,16 +339,13 @@ def cache_extend(cache: PagedCache, seqs: torch.Tensor, counts: torch.Tensor | N
     Returns ``starts`` (int32, written if given): the lengths before, where the
     new tokens go. All or nothing: where pages run out nothing changes, every
     start is -1 (which cache_write passes over) and check_device_status raises."""
-    c = cache._struct()
+    c, dev = _on_gpu(cache)
     n = seqs.numel()
-    lists = _list(cache, "seqs", seqs), _list(cache, "counts", counts, n)
+    at = _list(dev, "seqs", seqs), _list(dev, "counts", counts, n)
     if starts is None:
-        starts = torch.empty(n, dtype=torch.int32, device=cache.device)
-    at = _list(cache, "starts", starts, n)
-    ws = _workspace(workspace, cache_workspace_bytes(cache, n), cache.device)
-    with torch.cuda.device(cache.device):
-        _check_launch(_lib.bsmt_cache_extend(ctypes.byref(c), *lists, n, at, ws.data_ptr(), ws.numel(),
-                                             _stream_ptr(cache.device)))
+        starts = torch.empty(n, dtype=torch.int32, device=dev)
+    ws = _workspace(workspace, cache_workspace_bytes(cache, n), dev)
+    _call(dev, _lib.bsmt_cache_extend, c, *at, n, _list(dev, "starts", starts, n), ws.data_ptr(), ws.numel())
     return starts
 
 
@@ -352,22 +355,19 @@ def cache_write(cache: PagedCache, seqs: torch.Tensor, starts: torch.Tensor, k: 
     other strides multiples of 8) into the pages of sequences seqs from positions
     ``starts`` on, as cache_extend returned them. ``cu_seqlens`` (int32
     [n + 1]): the sequences' tokens in the pack; None: one token each."""
-    c = cache._struct()
+    c, dev = _on_gpu(cache)
     n = seqs.numel()
-    layers, _, heads, _, dim = cache.k.shape
+    _, _, heads, _, dim = cache.k.shape
     for name, t in (("k", k), ("v", v)):
-        if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1:] != (heads, dim) or t.device != cache.device:
-            raise ValueError(f"{name} must be bfloat16 [tokens, {heads}, {dim}] on {cache.device}")
-        if t.numel() > 0 and t.stride(2) != 1:
+        if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1:] != (heads, dim) or t.device != dev:
+            raise ValueError(f"{name} must be bfloat16 [tokens, {heads}, {dim}] on {dev}")
+        if t.stride(2) != 1 and t.numel() > 0:
             raise ValueError(f"{name}'s innermost dimension must be contiguous")
     if k.shape != v.shape:
         raise ValueError(f"shape mismatch: k {tuple(k.shape)}, v {tuple(v.shape)}")
-    lists = (_list(cache, "seqs", seqs), _list(cache, "starts", starts, n), n,
-             _list(cache, "cu_seqlens", cu_seqlens, n + 1))
-    ks, vs = (_i64 * 2)(k.stride(0), k.stride(1)), (_i64 * 2)(v.stride(0), v.stride(1))
-    with torch.cuda.device(cache.device):
-        _check_launch(_lib.bsmt_cache_write(ctypes.byref(c), int(layer), *lists, k.data_ptr(), v.data_ptr(),
-                                            k.shape[0], ks, vs, _stream_ptr(cache.device)))
+    _call(dev, _lib.bsmt_cache_write, c, int(layer), _list(dev, "seqs", seqs), _list(dev, "starts", starts, n), n,
+          _list(dev, "cu_seqlens", cu_seqlens, n + 1), k.data_ptr(), v.data_ptr(), k.shape[0],
+          _I64x2(k.stride(0), k.stride(1)), _I64x2(v.stride(0), v.stride(1)))
 
 
 def cache_gather(cache: PagedCache, seqs: torch.Tensor, starts: torch.Tensor | None, total: int,
@@ -377,55 +377,46 @@ def cache_gather(cache: PagedCache, seqs: torch.Tensor, starts: torch.Tensor | N
     pack is position starts[i] + t - cu_seqlens[i] of sequence seqs[i]
     (``starts`` None: from 0; ``cu_seqlens`` None: one token each). For a
     prompt that goes on from a cached part, flex_attention_varlen takes them."""
-    c = cache._struct()
+    c, dev = _on_gpu(cache)
     n = seqs.numel()
     _, _, heads, _, dim = cache.k.shape
-    lists = (_list(cache, "seqs", seqs), _list(cache, "starts", starts, n), n,
-             _list(cache, "cu_seqlens", cu_seqlens, n + 1))
     shape = (int(total), heads, dim)
-    k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
-    v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
+    if k is None:
+        k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    if v is None:
+        v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     for name, t in (("k", k), ("v", v)):
-        if t.shape != torch.Size(shape) or t.dtype != torch.bfloat16 or not t.is_contiguous() or t.device != cache.device:
-            raise ValueError(f"{name} must be a contiguous bf16 tensor {shape} on {cache.device}")
-    with torch.cuda.device(cache.device):
-        _check_launch(_lib.bsmt_cache_gather(ctypes.byref(c), int(layer), *lists, int(total), k.data_ptr(),
-                                             v.data_ptr(), _stream_ptr(cache.device)))
+        if t.shape != shape or t.dtype != torch.bfloat16 or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous bf16 tensor {shape} on {dev}")
+    _call(dev, _lib.bsmt_cache_gather, c, int(layer), _list(dev, "seqs", seqs), _list(dev, "starts", starts, n), n,
+          _list(dev, "cu_seqlens", cu_seqlens, n + 1), shape[0], k.data_ptr(), v.data_ptr())
     return k, v
 
 
 def cache_fork(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor, workspace: torch.Tensor | None = None) -> None:
     """Slot dst[i], empty before, becomes a copy of sequence src[i]: full pages
     are shared, a partial last page is copied. All or nothing, as cache_extend."""
-    c = cache._struct()
+    c, dev = _on_gpu(cache)
     n = src.numel()
-    lists = _list(cache, "src", src), _list(cache, "dst", dst, n)
-    ws = _workspace(workspace, cache_workspace_bytes(cache, n), cache.device)
-    with torch.cuda.device(cache.device):
-        _check_launch(_lib.bsmt_cache_fork(ctypes.byref(c), *lists, n, ws.data_ptr(), ws.numel(),
-                                           _stream_ptr(cache.device)))
+    ws = _workspace(workspace, cache_workspace_bytes(cache, n), dev)
+    _call(dev, _lib.bsmt_cache_fork, c, _list(dev, "src", src), _list(dev, "dst", dst, n), n, ws.data_ptr(), ws.numel())
 
 
 def cache_free(cache: PagedCache, seqs: torch.Tensor) -> None:
     """Empties sequences; pages that no other sequence holds become free."""
-    c = cache._struct()
-    at = _list(cache, "seqs", seqs)
-    with torch.cuda.device(cache.device):
-        _check_launch(_lib.bsmt_cache_free(ctypes.byref(c), at, seqs.numel(), _stream_ptr(cache.device)))
+    c, dev = _on_gpu(cache)
+    _call(dev, _lib.bsmt_cache_free, c, _list(dev, "seqs", seqs), seqs.numel())
 
 
 def cache_compact(cache: PagedCache, live: torch.Tensor | None = None,
                   workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Moves the pages in use to the front of the pool. Returns their number as
     an int32 [1] device tensor (``live``, written if given)."""
-    c = cache._struct()
+    c, dev = _on_gpu(cache)
     if live is None:
-        live = torch.empty(1, dtype=torch.int32, device=cache.device)
-    at = _list(cache, "live", live, 1)
-    ws = _workspace(workspace, cache_workspace_bytes(cache), cache.device)
-    with torch.cuda.device(cache.device):
-        _check_launch(_lib.bsmt_cache_compact(ctypes.byref(c), at, ws.data_ptr(), ws.numel(),
-                                              _stream_ptr(cache.device)))
+        live = torch.empty(1, dtype=torch.int32, device=dev)
+    ws = _workspace(workspace, cache_workspace_bytes(cache), dev)
+    _call(dev, _lib.bsmt_cache_compact, c, _list(dev, "live", live, 1), ws.data_ptr(), ws.numel())
     return live
 
 
@@ -433,8 +424,8 @@ def cache_compact(cache: PagedCache, live: torch.Tensor | None = None,
 def paged_attention_workspace_bytes(head_dim: int) -> int:
     """Bytes of device workspace paged_attention needs."""
     b = _i64(0)
-    _check(_lib.bsmt_paged_attention_workspace_bytes(int(head_dim), ctypes.byref(b)))
-    return int(b.value)
+    _check(_lib.bsmt_paged_attention_workspace_bytes(int(head_dim), _byref(b)))
+    return b.value
 
 
 def paged_attention(q: torch.Tensor, cache: PagedCache, seqs: torch.Tensor, cu_seqlens_q: torch.Tensor | None = None,
@@ -450,31 +441,29 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, seqs: torch.Tensor, cu_s
     several queries a sequence want causal(). Keys no query sees are not read.
     Returns (out bf16 [T, Hq, D], lse fp32 [Hq, T]); rows that see nothing get 0
     and -inf. No gradient flows to the cache."""
-    if q.dtype != torch.bfloat16 or q.dim() != 3 or not q.is_contiguous() or q.device != cache.device:
-        raise ValueError(f"q must be a contiguous bf16 tensor [tokens, Hq, D] on {cache.device}")
-    c = cache._struct()
+    c, device = _on_gpu(cache)
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.device != device or not q.is_contiguous():
+        raise ValueError(f"q must be a contiguous bf16 tensor [tokens, Hq, D] on {device}")
     T, Hq, D = q.shape
     if D != cache.k.shape[4]:
         raise ValueError(f"q has head dim {D}, the cache {cache.k.shape[4]}")
-    if torch.is_grad_enabled() and q.requires_grad:
+    if q.requires_grad and torch.is_grad_enabled():
         raise ValueError("paged_attention has no backward; detach q or use flex_attention_varlen")
     n = seqs.numel()
-    lists = _list(cache, "seqs", seqs), n, _list(cache, "cu_seqlens_q", cu_seqlens_q, n + 1)
-    device = cache.device
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((Hq, T), dtype=torch.float32, device=device) if lse is None else lse
-    if out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != device:
+    at = _list(device, "seqs", seqs), n, _list(device, "cu_seqlens_q", cu_seqlens_q, n + 1)
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != device:
         raise ValueError("out must be a contiguous bf16 tensor of q's shape and device")
-    if lse.shape != (Hq, T) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != device:
+    if lse is None:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=device)
+    elif lse.shape != (Hq, T) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != device:
         raise ValueError("lse must be a contiguous fp32 tensor [Hq, tokens] on q's device")
     ws = _workspace(workspace, paged_attention_workspace_bytes(D), device)
-    with torch.cuda.device(device):
-        mspec, keep_m = (None, []) if mask_mod is None else mask_mod._spec(device, 1)
-        sspec, keep_s = _score_spec(score_mod, device, Hq)
-        _check_launch(_lib.bsmt_paged_attention(
-            q.data_ptr(), T, Hq, ctypes.byref(c), int(layer), *lists,
-            ctypes.byref(mspec) if mspec is not None else None, ctypes.byref(sspec),
-            ctypes.c_float(0.0 if scale is None else float(scale)), int(bool(enable_gqa)), out.data_ptr(),
-            lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream_ptr(device)))
+    mspec, keep_m = (None, None) if mask_mod is None else mask_mod._spec(device, 1)
+    sspec, keep_s = _score_spec(score_mod, device, Hq)
+    _call(device, _lib.bsmt_paged_attention, q.data_ptr(), T, Hq, c, int(layer), *at,
+          None if mspec is None else _byref(mspec), _byref(sspec), 0.0 if scale is None else float(scale),
+          int(bool(enable_gqa)), out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel())
     del keep_m, keep_s
     return out, lse
