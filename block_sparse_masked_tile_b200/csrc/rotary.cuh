@@ -13,8 +13,10 @@
 // floating point. Its top 32 bits give the angle to sincospif, in half turns.
 //
 // Bound by HBM: x is read once and written once. A thread keeps the sines of
-// its eight pairs of one token in registers and goes over heads with them, so
-// the trigonometry is paid once for kRotaryHeads heads of q and k together.
+// its eight pairs of one token in registers and goes over heads of q and k with
+// them, one head's 32 bytes in and out at a time: more blocks on an SM hide the
+// reads better than more heads in one thread (two blocks with four heads each
+// 159 us, four with one 117 us, for 30011 tokens of 40 heads of 128).
 #pragma once
 #include <cstdint>
 
@@ -42,7 +44,7 @@ struct RotaryParams {
     const int32_t* pos;
     int64_t pos_axis, pos_b, pos_t;
     int64_t tokens;  // B * T
-    int32_t T, head_dim, pairs, heads, chunk, inverse;
+    int32_t T, head_dim, pairs, heads, chunk, side, inverse;
 };
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
@@ -63,7 +65,7 @@ __device__ __forceinline__ E* rotary_row(const RotaryParams& p, int h, int64_t b
 // VEC: pairs of one thread, 8 where every row is 16-byte aligned and the pair
 // count a multiple of 8, else 1. A load is at most 16 bytes.
 template <typename E, int VEC, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
+__global__ void __launch_bounds__(kRotaryThreads, 4) rotary_kernel(const __grid_constant__ RotaryParams p) {
     __shared__ uint64_t s_turn[BSMT_MAX_ROTARY_PAIRS];
     __shared__ int8_t s_axis[BSMT_MAX_ROTARY_PAIRS];
     for (int i = threadIdx.x; i < p.pairs; i += kRotaryThreads) {
@@ -75,9 +77,11 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
     constexpr int NL = VEC / L;
     const int groups = p.pairs / VEC;
     const int64_t unit = static_cast<int64_t>(blockIdx.x) * kRotaryThreads + threadIdx.x;
-    const int64_t token = unit / groups;
+    const int64_t lane_unit = unit / groups;  // (token, which of the heads that go side by side)
+    const int64_t token = lane_unit / p.side;
     if (token >= p.tokens) return;
-    const int first = static_cast<int>(unit - token * groups) * VEC;
+    const int first = static_cast<int>(unit - lane_unit * groups) * VEC;
+    const int side = static_cast<int>(lane_unit - token * p.side);
     const int64_t b = token / p.T, t = token - b * p.T;
 
     float cs[VEC], sn[VEC];
@@ -99,48 +103,35 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
     const int h1 = min(p.heads, static_cast<int>(blockIdx.y + 1) * p.chunk);
     const int at_a = INTERLEAVED ? 2 * first : first;
     const int at_b = INTERLEAVED ? 2 * first + VEC : p.pairs + first;  // (interleaved: the second half of 2 * VEC)
-    // kUnroll heads are loaded before the first is stored: out may be in itself,
-    // so the compiler keeps the order of what is written here.
-    constexpr int kUnroll = sizeof(E) == 2 ? 4 : 2;
-    for (int h0 = blockIdx.y * p.chunk; h0 < h1; h0 += kUnroll) {
-        Pack<E, L> va[kUnroll][NL], vb[kUnroll][NL];
+    for (int h = blockIdx.y * p.chunk + side; h < h1; h += p.side) {
+        const E* in = rotary_row<E>(p, h, b, t, false);
+        E* out = rotary_row<E>(p, h, b, t, true);
+        Pack<E, L> va[NL], vb[NL];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            if (h0 + u >= h1) break;
-            const E* in = rotary_row<E>(p, h0 + u, b, t, false);
+        for (int j = 0; j < NL; ++j) {
+            va[j] = *reinterpret_cast<const Pack<E, L>*>(in + at_a + j * L);
+            vb[j] = *reinterpret_cast<const Pack<E, L>*>(in + at_b + j * L);
+        }
+        Pack<E, L> ra[NL], rb[NL];
 #pragma unroll
-            for (int j = 0; j < NL; ++j) {
-                va[u][j] = *reinterpret_cast<const Pack<E, L>*>(in + at_a + j * L);
-                vb[u][j] = *reinterpret_cast<const Pack<E, L>*>(in + at_b + j * L);
-            }
+        for (int i = 0; i < VEC; ++i) {
+            // element e of the thread's 2 * VEC lies in va for e < VEC, else in vb
+            const int ea = INTERLEAVED ? 2 * i : i, eb = INTERLEAVED ? 2 * i + 1 : VEC + i;
+            const float a = to_f32(ea < VEC ? va[ea / L % NL].v[ea % L] : vb[(ea - VEC) / L % NL].v[ea % L]);
+            const float c = to_f32(eb < VEC ? va[eb / L % NL].v[eb % L] : vb[(eb - VEC) / L % NL].v[eb % L]);
+            E ya, yb;
+            from_f32(fmaf(a, cs[i], -(c * sn[i])), ya);
+            from_f32(fmaf(a, sn[i], c * cs[i]), yb);
+            (ea < VEC ? ra[ea / L % NL].v[ea % L] : rb[(ea - VEC) / L % NL].v[ea % L]) = ya;
+            (eb < VEC ? ra[eb / L % NL].v[eb % L] : rb[(eb - VEC) / L % NL].v[eb % L]) = yb;
         }
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            if (h0 + u >= h1) break;
-            Pack<E, L> ra[NL], rb[NL];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                // element e of the thread's 2 * VEC lies in va for e < VEC, else in vb
-                const int ea = INTERLEAVED ? 2 * i : i, eb = INTERLEAVED ? 2 * i + 1 : VEC + i;
-                const float a = to_f32(ea < VEC ? va[u][ea / L % NL].v[ea % L] : vb[u][(ea - VEC) / L % NL].v[ea % L]);
-                const float c = to_f32(eb < VEC ? va[u][eb / L % NL].v[eb % L] : vb[u][(eb - VEC) / L % NL].v[eb % L]);
-                E ya, yb;
-                from_f32(fmaf(a, cs[i], -(c * sn[i])), ya);
-                from_f32(fmaf(a, sn[i], c * cs[i]), yb);
-                (ea < VEC ? ra[ea / L % NL].v[ea % L] : rb[(ea - VEC) / L % NL].v[ea % L]) = ya;
-                (eb < VEC ? ra[eb / L % NL].v[eb % L] : rb[(eb - VEC) / L % NL].v[eb % L]) = yb;
-            }
-            E* out = rotary_row<E>(p, h0 + u, b, t, true);
-#pragma unroll
-            for (int j = 0; j < NL; ++j) {
-                *reinterpret_cast<Pack<E, L>*>(out + at_a + j * L) = ra[j];
-                *reinterpret_cast<Pack<E, L>*>(out + at_b + j * L) = rb[j];
-            }
-            if (2 * p.pairs < p.head_dim) {
-                const E* in = rotary_row<E>(p, h0 + u, b, t, false);
-                for (int e = 2 * p.pairs + first / VEC; e < p.head_dim; e += groups) out[e] = in[e];
-            }
+        for (int j = 0; j < NL; ++j) {
+            *reinterpret_cast<Pack<E, L>*>(out + at_a + j * L) = ra[j];
+            *reinterpret_cast<Pack<E, L>*>(out + at_b + j * L) = rb[j];
         }
+        if (2 * p.pairs < p.head_dim)
+            for (int e = 2 * p.pairs + first / VEC; e < p.head_dim; e += groups) out[e] = in[e];
     }
 }
 

@@ -143,22 +143,25 @@ def rotary_spec(head_dim: int, sections: Sequence[int] | None = None, base: floa
 
 def _heads_tokens(t: torch.Tensor) -> tuple:
     """(B, heads, T, strides of batch, head and token) of [T, H, D] or [B, H, T, D]."""
-    if t.dim() == 3:
-        return 1, t.shape[1], t.shape[0], (0, t.stride(1), t.stride(0))
-    return t.shape[0], t.shape[1], t.shape[2], (t.stride(0), t.stride(1), t.stride(2))
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        return 1, shape[1], shape[0], (0, stride[1], stride[0])
+    return shape[0], shape[1], shape[2], stride[:3]
 
 
 def _rotary(tensors, positions: torch.Tensor, spec: RotarySpec, inverse: bool) -> list:
     first = tensors[0]
-    dev = first.device
-    B, _, T, _ = _heads_tokens(first)
-    outs = [torch.empty(x.shape, dtype=x.dtype, device=dev) for x in tensors]
-    c = (_RotaryTensor * len(tensors))(*[
-        (x.data_ptr(), y.data_ptr(), _heads_tokens(x)[3], _heads_tokens(y)[3], x.shape[1]) for x, y in zip(tensors, outs)])
+    dev, dtype = first.device, first.dtype
+    outs, c = [], (_RotaryTensor * len(tensors))()
+    for i, x in enumerate(tensors):
+        y = torch.empty(x.shape, dtype=dtype, device=dev)
+        B, heads, T, strides = _heads_tokens(x)
+        c[i] = x.data_ptr(), y.data_ptr(), strides, _heads_tokens(y)[3], heads
+        outs.append(y)
     dims = positions.dim()
     strides = _I64x3(positions.stride(0) if dims > 1 else 0, positions.stride(1) if dims == 3 else 0,
                      positions.stride(dims - 1))
-    _call(dev, _lib.bsmt_rotary, _byref(spec._c), _ROTARY_DTYPES[first.dtype], B, T, positions.data_ptr(), strides,
+    _call(dev, _lib.bsmt_rotary, _byref(spec._c), _ROTARY_DTYPES[dtype], B, T, positions.data_ptr(), strides,
           int(inverse), c, len(tensors))
     return outs
 
@@ -181,7 +184,11 @@ class _RotaryFn(torch.autograd.Function):
         if at:
             # (a broadcast gradient, as of a sum, has stride 0 in its rows)
             some = [g if g.stride(-1) == 1 or g.shape[-1] == 1 else g.contiguous() for g in (grads[i] for i in at)]
-            for i, g in zip(at, _RotaryFn.apply(positions, spec, not inverse, *some)):
+            if torch.is_grad_enabled():  # (create_graph: the turn of the gradient is differentiable, too)
+                turned = _RotaryFn.apply(positions, spec, not inverse, *some)
+            else:
+                turned = _rotary(some, positions, spec, not inverse)
+            for i, g in zip(at, turned):
                 out[i] = g
         return (None, None, None, *out)
 
