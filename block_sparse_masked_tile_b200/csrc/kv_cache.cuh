@@ -13,6 +13,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "async_copy.cuh"
 #include "bsmt_serving.h"
 
 namespace bsmt {
@@ -35,8 +36,6 @@ struct alignas(sizeof(E) * N) Pack {
 };
 
 constexpr int kMinScaleExp = -120;  // a page of zeros has this scale
-
-__device__ __forceinline__ void set_status(int* status, int code) { atomicCAS(status, 0, code); }
 
 __device__ __forceinline__ int64_t page_elems(const KvCache& c) {
     return static_cast<int64_t>(c.heads) * c.page * c.dim;
@@ -92,7 +91,8 @@ template <bool INT8>
 __device__ __forceinline__ void decode4(uint32_t w, float out[4]) {
     if (INT8) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) out[i] = static_cast<float>(static_cast<int8_t>(w >> (8 * i)));
+        for (int i = 0; i < 4; ++i)  // the float 2^23 + (code + 128), less 2^23 + 128
+            out[i] = __uint_as_float(__byte_perm(w ^ 0x80808080u, 0x4B000000u, 0x7440 + i)) - 8388736.f;
     } else {
         const float2 a = half2_floats(e4m3x2_to_half2(w)), b = half2_floats(e4m3x2_to_half2(w >> 16));
         out[0] = a.x, out[1] = a.y, out[2] = b.x, out[3] = b.y;
@@ -109,7 +109,7 @@ struct CacheWriteParams {
     const __nv_bfloat16* v;
     int64_t kt, kh, vt, vh;  // element strides: token, head
     int64_t T, items;
-    int32_t n, layer;
+    int32_t n, layer, share;  // share: heads of k and v that one block of a prompt takes
     int* status;
 };
 
@@ -128,115 +128,219 @@ __device__ __forceinline__ int item_sequence(const int32_t* cu, int n, int shift
     return lo;
 }
 
-// One team of TEAM threads quantises what one call puts into one page, for one
-// head of k or of v: the largest magnitude first, then the codes (the second
-// read hits L1 or L2). Rows that the page held before are moved to the new
-// scale if it is larger. TEAM = 32 for calls of a few tokens a sequence (decoding:
-// one 128- or 256-byte row), 256 for prompts.
-//
-// Bound by HBM for prompts (2 bytes read, 1 written for each element), by
-// latency for single tokens.
-template <int TEAM, bool INT8>
-__global__ void __launch_bounds__(256) cache_write_kernel(const __grid_constant__ CacheWriteParams p) {
-    __shared__ uint32_t s_max[8];
-    constexpr int kTeams = 256 / TEAM;
-    const int lane = threadIdx.x % TEAM;
-    const KvCache& c = p.c;
-    // unit = (item, head, k or v), a team's own: the exits below are uniform over it
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kTeams + threadIdx.x / TEAM;
-    const int per_item = 2 * c.heads;
-    const int64_t item = unit / per_item;
-    if (item >= p.items) return;
-    const int sub = static_cast<int>(unit - item * per_item);
-    const bool is_v = sub >= c.heads;
-    const int head = is_v ? sub - c.heads : sub;
+// Where the tokens of one item go.
+struct CacheItem {
+    int64_t token;  // the first, in the call's pack
+    int64_t place;  // layer * pages + page
+    int row0, rows;
+};
 
+// False: nothing to write (an entry passed over, or one that is refused).
+__device__ __forceinline__ bool cache_item(const CacheWriteParams& p, int64_t item, bool report, CacheItem& out) {
+    const KvCache& c = p.c;
     const int i = p.cu == nullptr ? static_cast<int>(item) : item_sequence(p.cu, p.n, c.page_shift, item);
     const int64_t t0 = p.cu == nullptr ? item : __ldg(p.cu + i), t1 = p.cu == nullptr ? item + 1 : __ldg(p.cu + i + 1);
     const int seq = __ldg(p.seqs + i);
     const int64_t start = __ldg(p.starts + i);
     if (t0 < 0 || t1 < t0 || t1 > p.T) {
-        if (lane == 0) set_status(p.status, BSMT_ERR_DEVICE_PRECONDITION);
-        return;
+        if (report) set_status(p.status, BSMT_ERR_DEVICE_PRECONDITION);
+        return false;
     }
-    if (seq == -1 || start == -1 || t0 == t1) return;
+    if (seq == -1 || start == -1 || t0 == t1) return false;
     if (seq < 0 || seq >= c.max_seqs || start < 0 || start + (t1 - t0) > __ldg(c.seq_lens + seq) ||
         start + (t1 - t0) > seq_capacity(c)) {
-        if (lane == 0) set_status(p.status, BSMT_ERR_DEVICE_BOUNDS);
-        return;
+        if (report) set_status(p.status, BSMT_ERR_DEVICE_BOUNDS);
+        return false;
     }
     const int64_t which = p.cu == nullptr ? 0 : item - ((t0 >> c.page_shift) + 2 * static_cast<int64_t>(i));
     const int64_t slot = (start >> c.page_shift) + which;
     const int64_t lo = max(start, slot << c.page_shift), hi = min(start + (t1 - t0), (slot + 1) << c.page_shift);
-    if (which < 0 || lo >= hi) return;
+    if (which < 0 || lo >= hi) return false;
     const int page = __ldg(c.page_table + static_cast<int64_t>(seq) * c.max_pages + slot);
     if (page < 0 || page >= c.pages) {
-        if (lane == 0) set_status(p.status, BSMT_ERR_DEVICE_BOUNDS);
-        return;
+        if (report) set_status(p.status, BSMT_ERR_DEVICE_BOUNDS);
+        return false;
     }
     if (__ldg(c.ref_counts + page) != 1) {  // a page that others read, or a free one
-        if (lane == 0) set_status(p.status, BSMT_ERR_DEVICE_PRECONDITION);
-        return;
+        if (report) set_status(p.status, BSMT_ERR_DEVICE_PRECONDITION);
+        return false;
     }
-    const int row0 = static_cast<int>(lo & (c.page - 1)), rows = static_cast<int>(hi - lo);
-    const __nv_bfloat16* src = is_v ? p.v + (t0 + lo - start) * p.vt + head * p.vh : p.k + (t0 + lo - start) * p.kt + head * p.kh;
-    const int64_t src_row = is_v ? p.vt : p.kt;
-    const int64_t place = static_cast<int64_t>(p.layer) * c.pages + page;
-    uint8_t* dst = (is_v ? c.v : c.k) + place * page_elems(c) + static_cast<int64_t>(head) * c.page * c.dim;
-    float* scale = (is_v ? c.v_scale : c.k_scale) + place * c.heads + head;
-    const float held = row0 > 0 ? *scale : 0.f;
+    out.token = t0 + lo - start;
+    out.place = static_cast<int64_t>(p.layer) * c.pages + page;
+    out.row0 = static_cast<int>(lo & (c.page - 1));
+    out.rows = static_cast<int>(hi - lo);
+    return true;
+}
 
-    const int vecs = c.dim / 8, shift = c.dim == 128 ? 4 : 3;  // 16-byte vectors of a row
-    uint32_t most = 0;
-    bool nan = false;
-#pragma unroll 4
-    for (int x = lane; x < rows * vecs; x += TEAM) {
-        const uint4 w = *reinterpret_cast<const uint4*>(src + (x >> shift) * src_row + (x & (vecs - 1)) * 8);
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+// The largest magnitudes of a vector's even and odd values, as bf16 bits in two halves.
+__device__ __forceinline__ uint32_t most_of(const uint4& w, uint32_t most) {
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t a = ws[j] & 0x7FFFu, b = ws[j] >> 16 & 0x7FFFu;
-            most = max(most, max(a < 0x7F80u ? a : 0u, b < 0x7F80u ? b : 0u));  // finite values only
-            nan = nan || a > 0x7F80u || b > 0x7F80u;
-        }
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t a = ws[j] & 0x7FFF7FFFu;
+        asm("max.u16x2 %0, %0, %1;" : "+r"(most) : "r"(a));
     }
-    most = __reduce_max_sync(0xFFFFFFFFu, most);
-    if (TEAM > 32) {
-        if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = most;
-        __syncthreads();
+    return most;
+}
+
+// The same without infinities and NaN; notes whether there is a NaN.
+__device__ __forceinline__ uint32_t most_finite(const uint4& w, uint32_t most, bool& nan) {
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int w = 0; w < 8; ++w) most = max(most, s_max[w]);
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t a = ws[j] & 0x7FFFu, b = ws[j] >> 16 & 0x7FFFu;
+        nan = nan || a > 0x7F80u || b > 0x7F80u;
+        const uint32_t f = (a < 0x7F80u ? a : 0u) | (b < 0x7F80u ? b : 0u) << 16;
+        asm("max.u16x2 %0, %0, %1;" : "+r"(most) : "r"(f));
     }
-    if (INT8 && nan) set_status(p.status, BSMT_ERR_DEVICE_PRECONDITION);  // (int8 has no NaN: stored as 0)
-    __syncwarp();  // every lane has read the held scale
+    return most;
+}
+
+// Eight values times inv as codes. `plain`: all finite, within the codes' range.
+template <bool INT8>
+__device__ __forceinline__ uint2 encode8(const uint4& w, float inv, bool plain) {
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(ws[j] << 16);
+        f[2 * j + 1] = __uint_as_float(ws[j] & 0xFFFF0000u);
+    }
+    if (INT8 && plain) {
+        // x * inv + 1.5 * 2^23 rounds to the nearest whole number, ties to even, into the low bits (x * inv is exact)
+        uint32_t u[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(fmaf(f[j], inv, 12582912.f));
+        return make_uint2(__byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410),
+                          __byte_perm(__byte_perm(u[4], u[5], 0x0040), __byte_perm(u[6], u[7], 0x0040), 0x5410));
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] *= inv;
+    return make_uint2(encode4<INT8>(f[0], f[1], f[2], f[3]), encode4<INT8>(f[4], f[5], f[6], f[7]));
+}
+
+// The scale of a page's head once `most` is among its values, its inverse, and,
+// where the page holds rows already and the scale grows, those rows under it.
+template <bool INT8>
+__device__ __forceinline__ float page_scale(uint32_t most, float held, int row0, uint8_t* codes, int dim, int lane, int team,
+                                            float* inv) {
     const int e = scale_exp(most, INT8);
     const float fresh = exp2i(e);
     const float used = fmaxf(fresh, held);
-    const float inv = used == fresh ? exp2i(-e) : __fdiv_rn(1.f, used);
+    *inv = used == fresh ? exp2i(-e) : __fdiv_rn(1.f, used);
     if (row0 > 0 && used != held) {
         const float ratio = __fdiv_rn(held, used);
-        for (int x = lane; x < row0 * c.dim / 4; x += TEAM) {
-            uint32_t* w = reinterpret_cast<uint32_t*>(dst) + x;
+        for (int x = lane; x < row0 * dim / 4; x += team) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(codes) + x;
             float f[4];
             decode4<INT8>(*w, f);
             *w = encode4<INT8>(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
         }
     }
-    dst += static_cast<int64_t>(row0) * c.dim;
-#pragma unroll 4
-    for (int x = lane; x < rows * vecs; x += TEAM) {
-        const uint4 w = *reinterpret_cast<const uint4*>(src + (x >> shift) * src_row + (x & (vecs - 1)) * 8);
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f[2 * j] = __uint_as_float(ws[j] << 16) * inv;
-            f[2 * j + 1] = __uint_as_float(ws[j] & 0xFFFF0000u) * inv;
-        }
+    return used;
+}
+
+// A few tokens a sequence (decoding): a warp quantises what the call puts into one
+// page, for one head of k or of v (one 128- or 256-byte row for one token). The
+// largest magnitude first, then the codes; a second read of more rows than the
+// first loop keeps hits L1. Bound by the latency of the chain from the list to the page.
+template <bool INT8>
+__global__ void __launch_bounds__(256) cache_write_rows_kernel(const __grid_constant__ CacheWriteParams p) {
+    const int lane = threadIdx.x & 31;
+    const KvCache& c = p.c;
+    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);  // (item, k or v, head)
+    const int per_item = 2 * c.heads;
+    const int64_t item = unit / per_item;
+    CacheItem it;
+    if (item >= p.items || !cache_item(p, item, lane == 0, it)) return;
+    const int sub = static_cast<int>(unit - item * per_item);
+    const bool is_v = sub >= c.heads;
+    const int head = is_v ? sub - c.heads : sub;
+    const int64_t src_row = is_v ? p.vt : p.kt;
+    const __nv_bfloat16* src = (is_v ? p.v + head * p.vh : p.k + head * p.kh) + it.token * src_row;
+    uint8_t* dst = (is_v ? c.v : c.k) + it.place * page_elems(c) + static_cast<int64_t>(head) * c.page * c.dim;
+    float* scale = (is_v ? c.v_scale : c.k_scale) + it.place * c.heads + head;
+    const float held = it.row0 > 0 ? *scale : 0.f;
+    const int vecs = c.dim / 8, shift = c.dim == 128 ? 4 : 3;  // 16-byte vectors of a row
+    uint32_t both = 0;
+    bool nan = false;
+    for (int x = lane; x < it.rows * vecs; x += 32)
+        both = most_finite(*reinterpret_cast<const uint4*>(src + (x >> shift) * src_row + (x & (vecs - 1)) * 8), both, nan);
+    const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, max(both & 0xFFFFu, both >> 16));
+    if (INT8 && nan) set_status(p.status, BSMT_ERR_DEVICE_PRECONDITION);  // (int8 has no NaN: stored as 0)
+    __syncwarp();  // every lane has read the held scale
+    float inv;
+    const float used = page_scale<INT8>(most, held, it.row0, dst, c.dim, lane, 32, &inv);
+    dst += static_cast<int64_t>(it.row0) * c.dim;
+    for (int x = lane; x < it.rows * vecs; x += 32)
         *reinterpret_cast<uint2*>(dst + x * 8) =
-            make_uint2(encode4<INT8>(f[0], f[1], f[2], f[3]), encode4<INT8>(f[4], f[5], f[6], f[7]));
-    }
+            encode8<INT8>(*reinterpret_cast<const uint4*>(src + (x >> shift) * src_row + (x & (vecs - 1)) * 8), inv, false);
     if (lane == 0) *scale = used;
+}
+
+// Prompts: a block quantises what the call puts into one page, for `share` of the
+// 2 * Hkv heads of k and v, one after another. It finds the page once, holds a head's
+// values in registers (NV vectors of 8 a thread: a page is NV * 2048 values at most)
+// from the search for the largest to the codes, and has the next head's on their way
+// meanwhile. Bound by HBM: 2 bytes read, 1 written for each element.
+template <int NV, bool INT8>
+__global__ void __launch_bounds__(256) cache_write_pages_kernel(const __grid_constant__ CacheWriteParams p) {
+    __shared__ uint32_t s_most[2][8];
+    const KvCache& c = p.c;
+    const int groups = (2 * c.heads + p.share - 1) / p.share;
+    const int64_t item = blockIdx.x / groups;
+    CacheItem it;
+    if (!cache_item(p, item, threadIdx.x == 0, it)) return;
+    const int u0 = static_cast<int>(blockIdx.x - item * groups) * p.share, u1 = min(2 * c.heads, u0 + p.share);
+    const int vecs = c.dim / 8, shift = c.dim == 128 ? 4 : 3;
+    const int all = it.rows * vecs;
+    auto load = [&](int u, uint4 w[NV]) {
+        const bool is_v = u >= c.heads;
+        const int64_t src_row = is_v ? p.vt : p.kt;
+        const __nv_bfloat16* src = (is_v ? p.v + (u - c.heads) * p.vh : p.k + u * p.kh) + it.token * src_row;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int x = threadIdx.x + 256 * j;
+            w[j] = x < all ? *reinterpret_cast<const uint4*>(src + (x >> shift) * src_row + (x & (vecs - 1)) * 8) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    uint4 now[NV], next[NV];
+    load(u0, now);
+    for (int u = u0; u < u1; ++u) {
+        const bool is_v = u >= c.heads;
+        const int head = is_v ? u - c.heads : u;
+        uint8_t* dst = (is_v ? c.v : c.k) + it.place * page_elems(c) + static_cast<int64_t>(head) * c.page * c.dim;
+        float* scale = (is_v ? c.v_scale : c.k_scale) + it.place * c.heads + head;
+        const float held = it.row0 > 0 ? *scale : 0.f;
+        if (u + 1 < u1) load(u + 1, next);
+        uint32_t both = 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) both = most_of(now[j], both);
+        const bool plain = (both & 0xFFFFu) < 0x7F80u && both < 0x7F800000u;
+        if (!plain) {  // infinities or NaN among this thread's values
+            bool nan = false;
+            both = 0;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) both = most_finite(now[j], both, nan);
+            if (INT8 && nan) set_status(p.status, BSMT_ERR_DEVICE_PRECONDITION);  // (int8 has no NaN: stored as 0)
+        }
+        uint32_t most = __reduce_max_sync(0xFFFFFFFFu, max(both & 0xFFFFu, both >> 16));
+        if ((threadIdx.x & 31) == 0) s_most[u & 1][threadIdx.x >> 5] = most;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < 8; ++w) most = max(most, s_most[u & 1][w]);
+        float inv;
+        const float used = page_scale<INT8>(most, held, it.row0, dst, c.dim, threadIdx.x, 256, &inv);
+        dst += static_cast<int64_t>(it.row0) * c.dim;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int x = threadIdx.x + 256 * j;
+            if (x < all) *reinterpret_cast<uint2*>(dst + x * 8) = encode8<INT8>(now[j], inv, plain);
+        }
+        if (threadIdx.x == 0) *scale = used;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) now[j] = next[j];
+    }
 }
 
 // ----------------------------------------------------------------- gather
@@ -248,11 +352,11 @@ struct CacheGatherParams {
     __nv_bfloat16* k;
     __nv_bfloat16* v;
     int64_t T;
-    int32_t n, layer;
+    int32_t n, layer, tokens;  // tokens of one block
     int* status;
 };
 
-constexpr int kGatherTokens = 16;
+constexpr int kGatherTokens = 16;  // at most
 
 // code * 2^e in bf16 (exact while the value is in bf16's normal range: a code
 // has at most 8 significant bits).
@@ -271,14 +375,14 @@ __device__ __forceinline__ uint4 dequantise8(uint2 w, float scale) {
 }
 
 // k, v [T, Hkv, D] of tokens of the cache: token t of sequence i is position
-// starts[i] + t - cu[i]. A block finds the places of kGatherTokens tokens, then
-// streams their rows. Bound by HBM: 1 byte read, 2 written for each element.
+// starts[i] + t - cu[i]. A block finds the places of its tokens, then streams
+// their rows. Bound by HBM: 1 byte read, 2 written for each element.
 template <bool INT8>
 __global__ void __launch_bounds__(256) cache_gather_kernel(const __grid_constant__ CacheGatherParams p) {
     __shared__ int s_page[kGatherTokens], s_row[kGatherTokens];
     const KvCache& c = p.c;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * kGatherTokens;
-    if (threadIdx.x < kGatherTokens && first + threadIdx.x < p.T) {
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * p.tokens;
+    if (threadIdx.x < p.tokens && first + threadIdx.x < p.T) {
         const int64_t t = first + threadIdx.x;
         int i = static_cast<int>(t);
         int64_t begin = t;
@@ -321,27 +425,27 @@ __global__ void __launch_bounds__(256) cache_gather_kernel(const __grid_constant
         s_row[threadIdx.x] = row;
     }
     __syncthreads();
-    const int tokens = static_cast<int>(min(static_cast<int64_t>(kGatherTokens), p.T - first));
-    const int shift = c.dim == 128 ? 4 : 3, vecs = c.dim / 8;
-    const int per_token = c.heads * vecs;
-    const int total = tokens * per_token;
-    for (int which = 0; which < 2; ++which) {
-        const uint8_t* codes = which ? p.c.v : p.c.k;
-        const float* scales = which ? c.v_scale : c.k_scale;
-        __nv_bfloat16* out = (which ? p.v : p.k) + first * per_token * 8;
+    // 16 codes at a time, of k's rows and then of v's
+    const int tokens = static_cast<int>(min(static_cast<int64_t>(p.tokens), p.T - first));
+    const int shift = c.dim == 128 ? 3 : 2, per_token = c.heads << shift;
+    const int half = tokens * per_token;
 #pragma unroll 4
-        for (int x = threadIdx.x; x < total; x += 256) {
-            const int t = x / per_token, hv = x - t * per_token;
-            const int head = hv >> shift, vec = hv & (vecs - 1);
-            uint4 r = make_uint4(0, 0, 0, 0);
-            if (s_page[t] >= 0) {
-                const int64_t place = static_cast<int64_t>(p.layer) * c.pages + s_page[t];
-                const uint2 w = *reinterpret_cast<const uint2*>(
-                    codes + ((place * c.heads + head) * c.page + s_row[t]) * c.dim + vec * 8);
-                r = dequantise8<INT8>(w, __ldg(scales + place * c.heads + head));
-            }
-            *reinterpret_cast<uint4*>(out + static_cast<int64_t>(x) * 8) = r;
+    for (int x = threadIdx.x; x < 2 * half; x += 256) {
+        const bool is_v = x >= half;
+        const int y = is_v ? x - half : x;
+        const int t = static_cast<uint32_t>(y) / static_cast<uint32_t>(per_token), hv = y - t * per_token;
+        const int head = hv >> shift, vec = hv & ((1 << shift) - 1);
+        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+        if (s_page[t] >= 0) {
+            const int64_t place = (static_cast<int64_t>(p.layer) * c.pages + s_page[t]) * c.heads + head;
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>((is_v ? c.v : c.k) + (place * c.page + s_row[t]) * c.dim + vec * 16));
+            const float scale = __ldg((is_v ? c.v_scale : c.k_scale) + place);
+            lo = dequantise8<INT8>(make_uint2(w.x, w.y), scale);
+            hi = dequantise8<INT8>(make_uint2(w.z, w.w), scale);
         }
+        uint4* out = reinterpret_cast<uint4*>((is_v ? p.v : p.k) + (first * per_token + y) * 16);
+        out[0] = lo;
+        out[1] = hi;
     }
 }
 
@@ -505,7 +609,9 @@ __global__ void __launch_bounds__(kPlanThreads) cache_extend_kernel(const __grid
         s_have[threadIdx.x] = have;
         s_seq[threadIdx.x] = seq;
         __syncthreads();
+#pragma unroll 4
         for (int r = threadIdx.x; r < total; r += kPlanThreads) {
+            const int page = __ldcg(p.list + before + r);
             int lo = 0, hi = kPlanThreads - 1;  // the last sequence whose pages begin at or before r
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
@@ -514,7 +620,6 @@ __global__ void __launch_bounds__(kPlanThreads) cache_extend_kernel(const __grid
                 else
                     hi = mid - 1;
             }
-            const int page = p.list[before + r];
             c.page_table[static_cast<int64_t>(s_seq[lo]) * c.max_pages + s_have[lo] + r - s_off[lo]] = page;
             c.ref_counts[page] = 1;
         }
@@ -596,28 +701,6 @@ __global__ void __launch_bounds__(kPlanThreads) cache_fork_plan_kernel(const __g
     }
 }
 
-// Copies `units` spans of 16 bytes with the block's share of the grid's threads.
-template <typename F>
-__device__ __forceinline__ void copy_vectors(int64_t begin, int64_t end, F place) {
-    constexpr int kDeep = 8;  // 16-byte loads a thread has in flight
-    for (int64_t x0 = begin + threadIdx.x; x0 < end; x0 += static_cast<int64_t>(blockDim.x) * kDeep) {
-        uint4 v[kDeep];
-        const uint4* from;
-        uint4* to[kDeep];
-#pragma unroll
-        for (int j = 0; j < kDeep; ++j) {
-            const int64_t x = x0 + static_cast<int64_t>(j) * blockDim.x;
-            if (x < end) {
-                place(x, from, to[j]);
-                v[j] = *from;
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < kDeep; ++j)
-            if (x0 + static_cast<int64_t>(j) * blockDim.x < end) *to[j] = v[j];
-    }
-}
-
 // The children's table rows and the counts of the pages they share, and the
 // copies of the partial pages: the rows that hold tokens, in every layer.
 __global__ void __launch_bounds__(256) cache_fork_kernel(const __grid_constant__ CacheForkParams p) {
@@ -641,24 +724,31 @@ __global__ void __launch_bounds__(256) cache_fork_kernel(const __grid_constant__
     if (rows == 0) return;
     const int old = from[full], page = job.y;
     if (part == 0 && threadIdx.x == 0) to[full] = page;
-    // vectors: (layer, k or v, head, the page's first `rows` rows)
-    const int64_t per_head = static_cast<int64_t>(rows) * c.dim / 16;
-    const int64_t spans = static_cast<int64_t>(c.layers) * 2 * c.heads;
+    // a warp for each (layer, k or v, head): the page's first `rows` rows
+    const int spans = c.layers * 2 * c.heads, vectors = rows * c.dim / 16;
     const int64_t head_bytes = static_cast<int64_t>(c.page) * c.dim;
-    const int64_t all = spans * per_head, share = (all + p.blocks - 1) / p.blocks;
-    const int64_t begin = part * share;
-    copy_vectors(begin, min(all, begin + share), [&](int64_t x, const uint4*& a, uint4*& b) {
-        const int64_t span = x / per_head;
-        const int64_t lk = span / c.heads, head = span - lk * c.heads;
+    for (int span = part * 8 + (threadIdx.x >> 5); span < spans; span += p.blocks * 8) {
+        const int lk = span / c.heads, head = span - lk * c.heads;
         uint8_t* pool = (lk & 1) ? c.v : c.k;
-        const int64_t base = (lk >> 1) * c.pages, in = (x - span * per_head) * 16;
-        a = reinterpret_cast<const uint4*>(pool + ((base + old) * c.heads + head) * head_bytes + in);
-        b = reinterpret_cast<uint4*>(pool + ((base + page) * c.heads + head) * head_bytes + in);
-    });
-    for (int64_t x = part * 256 + threadIdx.x; x < spans; x += p.blocks * 256) {
-        const int64_t lk = x / c.heads, head = x - lk * c.heads;
+        const int64_t base = static_cast<int64_t>(lk >> 1) * c.pages;
+        const uint4* a = reinterpret_cast<const uint4*>(pool + ((base + old) * c.heads + head) * head_bytes);
+        uint4* b = reinterpret_cast<uint4*>(pool + ((base + page) * c.heads + head) * head_bytes);
+        constexpr int kDeep = 8;  // 16-byte loads a thread has in flight
+        for (int x0 = threadIdx.x & 31; x0 < vectors; x0 += 32 * kDeep) {
+            uint4 v[kDeep];
+#pragma unroll
+            for (int j = 0; j < kDeep; ++j)
+                if (x0 + 32 * j < vectors) v[j] = a[x0 + 32 * j];
+#pragma unroll
+            for (int j = 0; j < kDeep; ++j)
+                if (x0 + 32 * j < vectors) b[x0 + 32 * j] = v[j];
+        }
+    }
+    for (int x = part * 256 + threadIdx.x; x < spans; x += p.blocks * 256) {
+        const int lk = x / c.heads, head = x - lk * c.heads;
         float* scale = (lk & 1) ? c.v_scale : c.k_scale;
-        scale[((lk >> 1) * c.pages + page) * c.heads + head] = scale[((lk >> 1) * c.pages + old) * c.heads + head];
+        const int64_t base = static_cast<int64_t>(lk >> 1) * c.pages;
+        scale[(base + page) * c.heads + head] = scale[(base + old) * c.heads + head];
     }
 }
 
@@ -749,57 +839,94 @@ __global__ void __launch_bounds__(kPlanThreads) cache_compact_plan_kernel(const 
     }
 }
 
-constexpr int kCompactChunk = 16384;  // bytes a block copies at a time
+constexpr int kCompactChunk = 16384;  // bytes of one copy
+constexpr int kCompactSlots = 4;
+constexpr int kCompactSmem = kCompactChunk * kCompactSlots;
 
-// Moves the pages (bound by HBM: each byte read once and written once) and
-// renames them in the table.
-__global__ void __launch_bounds__(256) cache_compact_kernel(const __grid_constant__ CacheCompactParams p) {
+// Moves the pages and renames them in the table. One thread of a block runs a ring
+// of bulk copies, global to shared to global, four of 16 KB under way; the others
+// rename and move the scales. Bound by HBM: each byte is read once and written once.
+__global__ void __launch_bounds__(128) cache_compact_kernel(const __grid_constant__ CacheCompactParams p) {
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ __align__(8) uint64_t s_bars[kCompactSlots];
     const KvCache& c = p.c;
     const int live = p.header[0], movers = p.header[1];
     if (movers == 0) return;
-    for (int seq = blockIdx.x; seq < c.max_seqs; seq += gridDim.x) {
-        const int64_t len = c.seq_lens[seq];
-        if (len < 0 || len > seq_capacity(c)) {
-            if (threadIdx.x == 0) set_status(p.status, BSMT_ERR_DEVICE_BOUNDS);
-            continue;
-        }
-        const int held = static_cast<int>((len + c.page - 1) >> c.page_shift);
-        for (int x = threadIdx.x; x < held; x += 256) {
-            int32_t* entry = c.page_table + static_cast<int64_t>(seq) * c.max_pages + x;
-            const int page = *entry;
-            if (page < 0 || page >= c.pages) {
-                set_status(p.status, BSMT_ERR_DEVICE_BOUNDS);
-            } else if (page >= live) {
-                const int to = p.to[page];
-                if (to < 0)
-                    set_status(p.status, BSMT_ERR_DEVICE_PRECONDITION);  // a free page in a table row: left as it is
-                else
-                    *entry = to;
+    const int64_t spans = static_cast<int64_t>(c.layers) * 2;  // (layer, k or v)
+    if (threadIdx.x == 0) {
+        const uint32_t bars = shared_addr(s_bars), slots = shared_addr(ring);
+        for (int i = 0; i < kCompactSlots; ++i) bar_init(bars + 8 * i);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        const int64_t bytes = page_elems(c);
+        const int chunks = static_cast<int>((bytes + kCompactChunk - 1) / kCompactChunk);
+        const int64_t units = movers * spans * chunks;
+        auto find = [&](int64_t u, const uint8_t*& from, uint8_t*& to) -> uint32_t {
+            const int64_t span = u / chunks;
+            const int chunk = static_cast<int>(u - span * chunks);
+            const int64_t r = span / spans, lk = span - r * spans;
+            uint8_t* pool = ((lk & 1) ? c.v : c.k) + (lk >> 1) * c.pages * bytes + static_cast<int64_t>(chunk) * kCompactChunk;
+            from = pool + p.movers[r] * bytes;
+            to = pool + p.holes[r] * bytes;
+            return static_cast<uint32_t>(min(static_cast<int64_t>(kCompactChunk), bytes - static_cast<int64_t>(chunk) * kCompactChunk));
+        };
+        // load unit n, then store unit n - (slots - 2) that came meanwhile
+        constexpr int kLag = kCompactSlots - 2;
+        uint8_t* to_q[kCompactSlots];
+        uint32_t size_q[kCompactSlots];
+        int64_t n = 0;
+        for (int64_t u = blockIdx.x; ; u += gridDim.x, ++n) {
+            const bool more = u < units;
+            if (!more && u - static_cast<int64_t>(kLag) * gridDim.x >= units) break;
+#pragma unroll
+            for (int q = 0; q < kCompactSlots; ++q) {
+                if (more && n % kCompactSlots == q) {
+                    const uint8_t* from;
+                    size_q[q] = find(u, from, to_q[q]);
+                    bulk_wait_read<1>();  // the store from this slot, two stores ago, has left it
+                    bar_expect(bars + 8 * q, size_q[q]);
+                    bulk_load(slots + q * kCompactChunk, from, size_q[q], bars + 8 * q);
+                }
+            }
+            const int64_t done = n - kLag;
+            if (done < 0) continue;
+#pragma unroll
+            for (int q = 0; q < kCompactSlots; ++q) {
+                if (done % kCompactSlots == q && u - static_cast<int64_t>(kLag) * gridDim.x < units) {
+                    bar_wait(bars + 8 * q, static_cast<uint32_t>(done / kCompactSlots) & 1u, p.status);
+                    bulk_store(to_q[q], slots + q * kCompactChunk, size_q[q]);
+                }
             }
         }
-    }
-    const int64_t bytes = page_elems(c);
-    const int64_t chunks = (bytes + kCompactChunk - 1) / kCompactChunk;
-    const int64_t spans = static_cast<int64_t>(c.layers) * 2;
-    const int64_t units = movers * spans * chunks;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int64_t chunk = u % chunks, ls = u / chunks;
-        const int64_t lk = ls % spans;
-        const int r = static_cast<int>(ls / spans);
-        const int from = p.movers[r], to = p.holes[r];
-        const int64_t base = (lk >> 1) * c.pages;
-        uint8_t* pool = (lk & 1) ? c.v : c.k;
-        const uint4* a = reinterpret_cast<const uint4*>(pool + (base + from) * bytes);
-        uint4* b = reinterpret_cast<uint4*>(pool + (base + to) * bytes);
-        const int64_t begin = chunk * kCompactChunk / 16, end = min(bytes, (chunk + 1) * kCompactChunk) / 16;
-        copy_vectors(begin, end, [&](int64_t x, const uint4*& f, uint4*& t) {
-            f = a + x;
-            t = b + x;
-        });
-        if (chunk == 0) {
-            float* scale = (lk & 1) ? c.v_scale : c.k_scale;
-            for (int h = threadIdx.x; h < c.heads; h += 256)
-                scale[(base + to) * c.heads + h] = scale[(base + from) * c.heads + h];
+        bulk_wait_all();
+    } else if (threadIdx.x >= 32) {
+        const int tid = threadIdx.x - 32;
+        for (int seq = blockIdx.x; seq < c.max_seqs; seq += gridDim.x) {
+            const int64_t len = c.seq_lens[seq];
+            if (len < 0 || len > seq_capacity(c)) {
+                if (tid == 0) set_status(p.status, BSMT_ERR_DEVICE_BOUNDS);
+                continue;
+            }
+            const int held = static_cast<int>((len + c.page - 1) >> c.page_shift);
+            for (int x = tid; x < held; x += 96) {
+                int32_t* entry = c.page_table + static_cast<int64_t>(seq) * c.max_pages + x;
+                const int page = *entry;
+                if (page < 0 || page >= c.pages) {
+                    set_status(p.status, BSMT_ERR_DEVICE_BOUNDS);
+                } else if (page >= live) {
+                    const int to = p.to[page];
+                    if (to < 0)
+                        set_status(p.status, BSMT_ERR_DEVICE_PRECONDITION);  // a free page in a table row: left as it is
+                    else
+                        *entry = to;
+                }
+            }
+        }
+        const int64_t scales = movers * spans * c.heads;
+        for (int64_t x = static_cast<int64_t>(blockIdx.x) * 96 + tid; x < scales; x += static_cast<int64_t>(gridDim.x) * 96) {
+            const int64_t span = x / c.heads, head = x - span * c.heads;
+            const int64_t r = span / spans, lk = span - r * spans;
+            float* scale = ((lk & 1) ? c.v_scale : c.k_scale) + (lk >> 1) * c.pages * c.heads + head;
+            scale[static_cast<int64_t>(p.holes[r]) * c.heads] = scale[static_cast<int64_t>(p.movers[r]) * c.heads];
         }
     }
 }

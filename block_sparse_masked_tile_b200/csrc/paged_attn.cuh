@@ -34,11 +34,11 @@
 #pragma once
 #include <cstdint>
 
-#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "async_copy.cuh"
 #include "kv_cache.cuh"
 #include "mask_dnf.cuh"
 
@@ -81,47 +81,6 @@ struct PagedShape {
     static constexpr int kQ = kPagedWarps * kWarpBytes;
     static constexpr int kSmem = kQ + (NT > 1 ? NT * (D / 16) * 256 : 0) + 1024;  // NT > 1: q's fragments; alignment
 };
-
-__device__ __forceinline__ uint32_t shared_addr(const void* p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-// Rows [row, row + box) of a pool into a slot; the slot's barrier counts the bytes.
-__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void bar_init(uint32_t bar) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// Waits for a slot. A load that does not come within 2 s is reported
-// (BSMT_ERR_DEVICE_TIMEOUT) and the kernel goes on to its end.
-__device__ __forceinline__ void bar_wait(uint32_t bar, uint32_t parity, int* status) {
-    if (bar_try(bar, parity)) return;
-    uint64_t t0, now;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-    while (!bar_try(bar, parity)) {
-        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-        if (now - t0 > 2000000000ull) {
-            set_status(status, BSMT_ERR_DEVICE_TIMEOUT);
-            return;
-        }
-    }
-}
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 r;

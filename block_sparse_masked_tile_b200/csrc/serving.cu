@@ -20,6 +20,11 @@ using namespace bsmt_host;
 
 namespace {
 
+// Kernels whose shared memory size has been raised on a device.
+std::mutex g_set_mu;
+bool g_paged_set[64][24] = {{false}};
+bool g_compact_set[64] = {false};
+
 constexpr int kMaxSeqs = 1 << 18;  // one bit each in the page planners' shared memory
 constexpr int kMaxPartBlocks = 1024;
 
@@ -215,6 +220,20 @@ extern "C" bsmt_status bsmt_rotary(const bsmt_rotary_spec* spec, int32_t dtype, 
 }
 
 // ------------------------------------------------------------------- cache
+namespace {
+template <bool INT8>
+void launch_write_pages(int nv, unsigned grid, cudaStream_t s, const bsmt::CacheWriteParams& p) {
+    if (nv <= 1)
+        bsmt::cache_write_pages_kernel<1, INT8><<<grid, 256, 0, s>>>(p);
+    else if (nv == 2)
+        bsmt::cache_write_pages_kernel<2, INT8><<<grid, 256, 0, s>>>(p);
+    else if (nv == 4)
+        bsmt::cache_write_pages_kernel<4, INT8><<<grid, 256, 0, s>>>(p);
+    else
+        bsmt::cache_write_pages_kernel<8, INT8><<<grid, 256, 0, s>>>(p);
+}
+}  // namespace
+
 extern "C" bsmt_status bsmt_cache_write(const bsmt_kv_cache* cache, int32_t layer, const int32_t* seqs, const int32_t* starts,
                                         int64_t n, const int32_t* cu_seqlens, const void* k, const void* v, int64_t T,
                                         const int64_t k_strides[2], const int64_t v_strides[2], void* stream) {
@@ -246,23 +265,28 @@ extern "C" bsmt_status bsmt_cache_write(const bsmt_kv_cache* cache, int32_t laye
     p.n = static_cast<int32_t>(n);
     p.layer = layer;
     p.items = cu_seqlens == nullptr ? n : (T >> p.c.page_shift) + 2 * n;
-    // A warp for calls of at most four tokens a sequence on average, a block of 256 otherwise.
-    const bool small = T <= 4 * n;
-    const int64_t units = p.items * 2 * p.c.heads;
-    const int64_t blocks = small ? (units + 7) / 8 : units;
-    if (blocks > 0x7FFFFFFF) return fail(BSMT_ERR_UNSUPPORTED, "cache_write: grid too large");
+    // A warp for each page, head and tensor in calls of at most four tokens a sequence on average, else a block for each
+    // page and some of the heads: few enough that there are 8 blocks an SM.
+    const bool few = T <= 4 * n;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const unsigned grid = static_cast<unsigned>(blocks);
-    if (p.c.int8) {
-        if (small)
-            bsmt::cache_write_kernel<32, true><<<grid, 256, 0, s>>>(p);
+    if (few) {
+        const int64_t blocks = (p.items * 2 * p.c.heads + 7) / 8;
+        if (blocks > 0x7FFFFFFF) return fail(BSMT_ERR_UNSUPPORTED, "cache_write: grid too large");
+        if (p.c.int8)
+            bsmt::cache_write_rows_kernel<true><<<static_cast<unsigned>(blocks), 256, 0, s>>>(p);
         else
-            bsmt::cache_write_kernel<256, true><<<grid, 256, 0, s>>>(p);
+            bsmt::cache_write_rows_kernel<false><<<static_cast<unsigned>(blocks), 256, 0, s>>>(p);
     } else {
-        if (small)
-            bsmt::cache_write_kernel<32, false><<<grid, 256, 0, s>>>(p);
+        const int64_t heads = 2 * int64_t(p.c.heads);
+        p.share = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(heads, p.items * heads / (8 * int64_t(nsm)))));
+        const int64_t blocks = p.items * ((heads + p.share - 1) / p.share);
+        if (blocks > 0x7FFFFFFF) return fail(BSMT_ERR_UNSUPPORTED, "cache_write: grid too large");
+        const unsigned grid = static_cast<unsigned>(blocks);
+        const int nv = p.c.page * p.c.dim / 2048;  // vectors of 8 values a thread holds
+        if (p.c.int8)
+            launch_write_pages<true>(nv, grid, s, p);
         else
-            bsmt::cache_write_kernel<256, false><<<grid, 256, 0, s>>>(p);
+            launch_write_pages<false>(nv, grid, s, p);
     }
     TRY(launched("cache_write"));
     return ok();
@@ -290,7 +314,9 @@ extern "C" bsmt_status bsmt_cache_gather(const bsmt_kv_cache* cache, int32_t lay
     p.T = T;
     p.n = static_cast<int32_t>(n);
     p.layer = layer;
-    const unsigned grid = static_cast<unsigned>((T + bsmt::kGatherTokens - 1) / bsmt::kGatherTokens);
+    // Tokens of a block: few enough for 4 blocks an SM, since each finds its tokens' places first.
+    p.tokens = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(bsmt::kGatherTokens, T / (4 * int64_t(nsm)))));
+    const unsigned grid = static_cast<unsigned>((T + p.tokens - 1) / p.tokens);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (p.c.int8)
         bsmt::cache_gather_kernel<true><<<grid, 256, 0, s>>>(p);
@@ -352,9 +378,9 @@ extern "C" bsmt_status bsmt_cache_fork(const bsmt_kv_cache* cache, const int32_t
     p.list = static_cast<int32_t*>(workspace);
     p.jobs = reinterpret_cast<int2*>(static_cast<char*>(workspace) + round256(int64_t(p.c.pages) * 4));
     p.n = static_cast<int32_t>(n);
-    // Blocks of one fork: 32 KB of a whole page's codes each, and some 8 blocks an SM in all.
-    const int64_t most = int64_t(p.c.layers) * 2 * p.c.heads * p.c.page * p.c.dim;
-    p.blocks = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>((most + 32767) / 32768, std::max<int64_t>(2, 8 * int64_t(nsm) / n))));
+    // Blocks of one fork: a warp for each head of k and v of a layer, and some 8 blocks an SM in all.
+    const int64_t spans = int64_t(p.c.layers) * 2 * p.c.heads;
+    p.blocks = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>((spans + 7) / 8, std::max<int64_t>(2, 8 * int64_t(nsm) / n))));
     const int bitmap = (p.c.max_seqs + 31) / 32 * 4;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     bsmt::cache_fork_plan_kernel<<<1, bsmt::kPlanThreads, bitmap, s>>>(p);
@@ -397,7 +423,15 @@ extern "C" bsmt_status bsmt_cache_compact(const bsmt_kv_cache* cache, int32_t* l
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     bsmt::cache_compact_plan_kernel<<<1, bsmt::kPlanThreads, 0, s>>>(p);
     TRY(launched("cache_compact plan"));
-    bsmt::cache_compact_kernel<<<4 * nsm, 256, 0, s>>>(p);
+    {
+        std::lock_guard<std::mutex> lk(g_set_mu);
+        if (!g_compact_set[dev]) {
+            const cudaError_t e = cudaFuncSetAttribute(bsmt::cache_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bsmt::kCompactSmem);
+            if (e != cudaSuccess) return fail(BSMT_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+            g_compact_set[dev] = true;
+        }
+    }
+    bsmt::cache_compact_kernel<<<3 * nsm, 128, bsmt::kCompactSmem, s>>>(p);
     TRY(launched("cache_compact"));
     return ok();
 }
@@ -405,8 +439,6 @@ extern "C" bsmt_status bsmt_cache_compact(const bsmt_kv_cache* cache, int32_t* l
 // --------------------------------------------------------------- attention
 namespace {
 
-std::mutex g_paged_mu;
-bool g_paged_set[64][24] = {{false}};
 
 // O, the maxima and sums of two parts for each block, and the blocks' heads.
 int64_t paged_ws_bytes(int64_t D) {
@@ -418,7 +450,7 @@ bsmt_status launch_paged(int dev, int nsm, bsmt::PagedParams p, const bsmt::Mask
     auto kern = bsmt::paged_attention_kernel<D, INT8, NT, MODS>;
     constexpr int smem = bsmt::PagedShape<D, NT>::kSmem;
     {
-        std::lock_guard<std::mutex> lk(g_paged_mu);
+        std::lock_guard<std::mutex> lk(g_set_mu);
         bool& set = g_paged_set[dev][(D == 128 ? 12 : 0) + (INT8 ? 6 : 0) + (NT / 2) * 2 + (MODS ? 1 : 0)];
         if (!set) {
             const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
