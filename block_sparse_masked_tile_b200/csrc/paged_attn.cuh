@@ -105,6 +105,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // A word's codes 0, 1 as the halves lo and codes 2, 3 as hi. The int8 codes come
 // with their top bit flipped (u = code + 128): the half 0x6400 | u is 1024 + u.
 template <bool INT8>
@@ -403,6 +409,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
                 if (tok < 0 || tok >= len) return -1;
                 return __ldg(table + (tok >> c.page_shift));
             };
+            // the page of the tile's second half: another one with pages of 16
+            auto second_page = [&](int tok, int first) -> int { return c.page == 16 ? page_at(tok < 0 ? -1 : tok + 16) : first; };
             int next_ord = t0 + warp;  // (after the first loads: the tile that find_next has found)
             int next_tok = -1, next_a = -1, next_b = -1;
             int tok_q[Shape::kDeep];      // first tokens of the tiles on their way
@@ -439,7 +447,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
                 for (int x = 0; x <= Shape::kDeep; ++x) {
                     first_tok[x] = tile_of(next_ord + x * kPagedWarps);
                     first_a[x] = page_at(first_tok[x]);
-                    first_b[x] = page_at(first_tok[x] < 0 ? -1 : first_tok[x] + 16);
+                    first_b[x] = second_page(first_tok[x], first_a[x]);
                 }
                 uint32_t slot = slot_k, bar = bar_k;
 #pragma unroll
@@ -601,7 +609,19 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
                                 }
                             }
                     }
-                    if (MODS) {
+                    if (MODS && !p.alibi) {
+                        // cap * tanh(z / cap), tanh(u) = 1 - 2 / (exp(2 u) + 1), in units of log2
+                        const float cap2 = p.cap * kLog2e;
+#pragma unroll
+                        for (int r = 0; r < NT; ++r)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float u = exp2_fast(s[r][h][e] * (qs[r][e & 1] * ks[h] * (2.f * kLog2e / p.cap)));
+                                    s[r][h][e] = fmaf(-2.f * cap2, rcp_fast(u + 1.f), cap2);
+                                }
+                    } else if (MODS) {
                         const int rel = tok - pos[0][0] + tok_g;
 #pragma unroll
                         for (int r = 0; r < NT; ++r)
@@ -611,11 +631,9 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
                                 for (int e = 0; e < 4; ++e) {
                                     const int y = e & 1;
                                     float z = s[r][h][e] * (qs[r][y] * ks[h]);
-                                    const float bias = slope[r][y] * static_cast<float>(rel + 16 * h + 8 * (e >> 1) -
-                                                                                        (pos[r][y] - pos[0][0]));
+                                    const float bias = slope[r][y] * static_cast<float>(rel + 16 * h + 8 * (e >> 1) - (pos[r][y] - pos[0][0]));
                                     if (p.alibi_first) z += bias;
-                                    // cap * tanh(z / cap), tanh(u) = 1 - 2 / (exp(2 u) + 1)
-                                    if (p.softcap) z = p.cap * (1.f - __fdividef(2.f, exp2_fast(z * (2.f * kLog2e / p.cap)) + 1.f));
+                                    if (p.softcap) z = p.cap * (1.f - 2.f * rcp_fast(exp2_fast(z * (2.f * kLog2e / p.cap)) + 1.f));
                                     if (!p.alibi_first) z += bias;
                                     s[r][h][e] = z * kLog2e;
                                 }
@@ -684,7 +702,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
                     begin_tile(Shape::kDeep - 1, slot_k, bar_k);
                     next_ord += kPagedWarps;
                     const int found = tile_of(next_ord);
-                    find_next(found, page_at(found), page_at(found < 0 ? -1 : found + 16));
+                    const int found_a = page_at(found);
+                    find_next(found, found_a, second_page(found, found_a));
                     uint32_t pb[NT][2][2];
 #pragma unroll
                     for (int r = 0; r < NT; ++r) {
