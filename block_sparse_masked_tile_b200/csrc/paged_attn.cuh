@@ -44,8 +44,7 @@
 
 namespace bsmt {
 
-constexpr int kPagedWarps = 4;
-constexpr int kPagedThreads = 32 * kPagedWarps;
+constexpr int kCombineWarps = 4;
 constexpr int kTileTokens = 32;
 constexpr float kLazy = 8.f;  // log2 by which a score may pass its reference: P stays below 2^8, far inside a half
 
@@ -63,22 +62,25 @@ struct PagedParams {
     int64_t T;
     int32_t n, layer, Hq, group, min_share;
     float scale, cap;
-    int32_t alibi, alibi_first, alibi_h0, alibi_heads, softcap;
+    int32_t alibi_first, alibi_h0, alibi_heads, softcap;
     int* status;
 };
 
-// Up to 32 registers of O a thread (NT * D <= 128): three blocks an SM with 16 KB of
-// slots a warp; more: two blocks, 24 KB a warp (three, with spills, took 1.4 times as
-// long at NT = 2). A slot holds the K or the V codes of a tile.
+// Three blocks an SM with 16 KB of slots a warp; with NT = 4 (D = 64 alone) two with
+// 24 KB. (NT = 2 at D = 128 has 168 registers and
+// some spills in three blocks, none in two: 338 and 378 us for 24 sequences up to
+// 64k with 16 rows each; five warps in two blocks 401 us.) A slot holds the K or the V
+// codes of a tile.
 template <int D, int NT>
 struct PagedShape {
-    static constexpr int kBlocks = NT * D > 128 ? 2 : 3;  // of an SM
+    static constexpr int kBlocks = NT > 2 ? 2 : 3;  // of an SM
+    static constexpr int kWarps = 4;
     static constexpr int kSlot = kTileTokens * D;
     static constexpr int kDeep = (kBlocks == 2 ? 3 : 2) * (128 / D);  // tiles a warp has loaded or on their way
     static constexpr int kWarpBytes = 2 * kDeep * kSlot;
     static constexpr int kPitch = D + 4;  // floats of a row where the warps' parts meet (in the slots)
     static_assert(8 * NT * (kPitch + 4) * 4 <= kWarpBytes, "a warp's part fits its slots");
-    static constexpr int kQ = kPagedWarps * kWarpBytes;
+    static constexpr int kQ = kWarps * kWarpBytes;
     static constexpr int kSmem = kQ + (NT > 1 ? NT * (D / 16) * 256 : 0) + 1024;  // NT > 1: q's fragments; alignment
 };
 
@@ -237,11 +239,13 @@ __device__ __forceinline__ int64_t paged_weight(const PagedParams& p, const Page
     return row_tiles * p.c.heads * (max(tiles, 1) + kUnitCost);
 }
 
-template <int D, bool INT8, int NT, bool MODS>
-__global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
+// MODS: 0 none, 1 soft-cap, 2 ALiBi with or without soft-cap.
+template <int D, bool INT8, int NT, int MODS>
+__global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, NT>::kBlocks)
     paged_attention_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ MaskDnf dnf,
                            const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using Shape = PagedShape<D, NT>;
+    constexpr int kWarps = Shape::kWarps, kBlockThreads = 32 * kWarps;
     constexpr int kSteps = D / 16;   // MMA steps over the head dimension
     constexpr int kChunks = D / 64;  // 16-byte pieces of a K row that one lane holds
     constexpr int kOut = D / 16;     // output tiles of 16 columns of V
@@ -250,8 +254,8 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
     constexpr float kLog2e = 1.4426950408889634f;
     constexpr float kLn2 = 0.6931471805599453f;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t s_bars[kPagedWarps * 2 * Shape::kDeep];
-    __shared__ long long s_scan[kPagedWarps];
+    __shared__ __align__(8) uint64_t s_bars[kWarps * 2 * Shape::kDeep];
+    __shared__ long long s_scan[kWarps];
     __shared__ long long s_off;
     __shared__ int s_i;
     __shared__ PagedSeqShared s_seq;
@@ -265,7 +269,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 
     // ---- this block's share of all tiles
-    const int per_thread = (p.n + kPagedThreads - 1) / kPagedThreads;
+    const int per_thread = (p.n + kBlockThreads - 1) / kBlockThreads;
     const int i_lo = min(p.n, tid * per_thread), i_hi = min(p.n, i_lo + per_thread);
     auto describe = [&](const PagedSeq& s) {  // what the whole block needs of a sequence
         s_seq.s = s;
@@ -298,7 +302,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
     __syncthreads();
     long long all = 0, before = incl - mine;
 #pragma unroll
-    for (int w = 0; w < kPagedWarps; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
         all += s_scan[w];
         if (w < warp) before += s_scan[w];
     }
@@ -329,12 +333,12 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
     if (p.cu != nullptr) {
         const int64_t used = max(0, min(__ldg(p.cu + p.n), static_cast<int>(p.T)));
         if (used < p.T) {
-            const int64_t stride = static_cast<int64_t>(gridDim.x) * kPagedThreads;
+            const int64_t stride = static_cast<int64_t>(gridDim.x) * kBlockThreads;
             const int64_t rest = (p.T - used) * p.Hq;
             uint4* o = reinterpret_cast<uint4*>(p.out + used * p.Hq * D);
-            for (int64_t x = static_cast<int64_t>(blockIdx.x) * kPagedThreads + tid; x < rest * (D / 8); x += stride)
+            for (int64_t x = static_cast<int64_t>(blockIdx.x) * kBlockThreads + tid; x < rest * (D / 8); x += stride)
                 o[x] = make_uint4(0, 0, 0, 0);
-            for (int64_t x = static_cast<int64_t>(blockIdx.x) * kPagedThreads + tid; x < rest; x += stride)
+            for (int64_t x = static_cast<int64_t>(blockIdx.x) * kBlockThreads + tid; x < rest; x += stride)
                 p.lse[x / (p.T - used) * p.T + used + x % (p.T - used)] = -INFINITY;
         }
     }
@@ -445,7 +449,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
                 int first_tok[Shape::kDeep + 1], first_a[Shape::kDeep + 1], first_b[Shape::kDeep + 1];  // (read together)
 #pragma unroll
                 for (int x = 0; x <= Shape::kDeep; ++x) {
-                    first_tok[x] = tile_of(next_ord + x * kPagedWarps);
+                    first_tok[x] = tile_of(next_ord + x * kWarps);
                     first_a[x] = page_at(first_tok[x]);
                     first_b[x] = second_page(first_tok[x], first_a[x]);
                 }
@@ -461,13 +465,17 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
                     bar = bar + 16 == bars + 16 * Shape::kDeep ? bars : bar + 16;
                 }
                 find_next(first_tok[Shape::kDeep], first_a[Shape::kDeep], first_b[Shape::kDeep]);
-                next_ord += Shape::kDeep * kPagedWarps;
+                next_ord += Shape::kDeep * kWarps;
             }
 
             // ---- q: row g of each 8, in halves; what the softmax needs of rows 2 t and 2 t + 1
             uint32_t qf[kQShared ? 1 : NT][kSteps][2];
-            float qs[NT][2], slope[NT][2];
-            int pos[NT][2];
+            float qs[NT][2], slope[MODS == 2 ? NT : 1][2];
+            auto pos_of = [&](int r, int y) {  // position of the query of row 8 r + 2 t + y
+                return len - count + static_cast<int>(qi0) +
+                       static_cast<int>(static_cast<uint32_t>(in_group + 8 * r + 2 * t + y) / static_cast<uint32_t>(p.group));
+            };
+            int pos[MODS == 2 ? NT : 1][2];
             const uint32_t q_smem = shared_addr(smem) + Shape::kQ + lane * 8;
 #pragma unroll
             for (int r = 0; r < NT; ++r) {
@@ -497,7 +505,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
                 most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
                 // largest value to [2^14, 2^15): the row's small values keep their bits, too
                 const int e = max(static_cast<int>(most >> 7) - 127, -100) - 14;
-                const float row_scale = exp2i(e) * p.scale * (MODS ? 1.f : kLog2e);
+                const float row_scale = exp2i(e) * p.scale * (MODS != 0 ? 1.f : kLog2e);
                 const float up = exp2i(-e);
 #pragma unroll
                 for (int x = 0; x < kChunks; ++x)
@@ -518,34 +526,35 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
                     }
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const int col = 8 * r + 2 * t + y;
-                    const int up_c = static_cast<int>(static_cast<uint32_t>(in_group + col) / static_cast<uint32_t>(p.group));
                     qs[r][y] = __shfl_sync(0xFFFFFFFFu, row_scale, (2 * t + y) * 4);
-                    pos[r][y] = len - count + static_cast<int>(qi0) + up_c;
-                    slope[r][y] = 0.f;
-                    if (MODS && p.alibi && row0 + col < rows_all) {
-                        const int h = head * p.group + in_group + col - up_c * p.group;
-                        slope[r][y] = p.slopes != nullptr
-                                          ? __ldg(p.slopes + h)
-                                          : exp2f(-8.f * static_cast<float>(p.alibi_h0 + h + 1) / static_cast<float>(p.alibi_heads));
+                    if (MODS == 2) {
+                        const int col = 8 * r + 2 * t + y;
+                        pos[r][y] = pos_of(r, y);
+                        slope[r][y] = 0.f;
+                        if (row0 + col < rows_all) {
+                            const int h = head * p.group + in_group + col - (pos[r][y] - (len - count) - static_cast<int>(qi0)) * p.group;
+                            slope[r][y] = p.slopes != nullptr
+                                              ? __ldg(p.slopes + h)
+                                              : exp2f(-8.f * static_cast<float>(p.alibi_h0 + h + 1) / static_cast<float>(p.alibi_heads));
+                        }
                     }
                 }
             }
             if (kQShared) __syncthreads();
 
             float o[NT][kOut][4];
-            float m[NT][2], mo[NT][2], l[NT][2], shift[NT][2];  // shift: 2^(m - mo)
+            float m[NT][2], mo[NT][2], l[NT][2];
 #pragma unroll
             for (int r = 0; r < NT; ++r) {
 #pragma unroll
-                for (int y = 0; y < 2; ++y) m[r][y] = mo[r][y] = -INFINITY, l[r][y] = shift[r][y] = 0.f;
+                for (int y = 0; y < 2; ++y) m[r][y] = mo[r][y] = -INFINITY, l[r][y] = 0.f;
 #pragma unroll
                 for (int x = 0; x < kOut; ++x)
 #pragma unroll
                     for (int y = 0; y < 4; ++y) o[r][x][y] = 0.f;
             }
 
-            for (int ord = t0 + warp; ord < t1; ord += kPagedWarps) {
+            for (int ord = t0 + warp; ord < t1; ord += kWarps) {
                 const int tok = tok_q[0];
                 if (tok >= 0) {
                     // s[r][h][2 z + y]: token 16 h + 8 z + tok_g, row 8 r + 2 t + y
@@ -601,15 +610,16 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
                         for (int r = 0; r < NT; ++r)
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
+                                const int at = pos_of(r, y);
                                 bits[r][y] = 0;
                                 for (int x = 0; x < dnf.n_terms; ++x) {
                                     int64_t lo, hi;
-                                    term_interval(dnf, x, pos[r][y], 0, len - 1, 0, 0, lo, hi);
+                                    term_interval(dnf, x, at, 0, len - 1, 0, 0, lo, hi);
                                     bits[r][y] |= range_bits(lo, hi, tok);
                                 }
                             }
                     }
-                    if (MODS && !p.alibi) {
+                    if (MODS == 1) {
                         // cap * tanh(z / cap), tanh(u) = 1 - 2 / (exp(2 u) + 1), in units of log2
                         const float cap2 = p.cap * kLog2e;
 #pragma unroll
@@ -621,7 +631,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
                                     const float u = exp2_fast(s[r][h][e] * (qs[r][e & 1] * ks[h] * (2.f * kLog2e / p.cap)));
                                     s[r][h][e] = fmaf(-2.f * cap2, rcp_fast(u + 1.f), cap2);
                                 }
-                    } else if (MODS) {
+                    } else if (MODS == 2) {
                         const int rel = tok - pos[0][0] + tok_g;
 #pragma unroll
                         for (int r = 0; r < NT; ++r)
@@ -658,7 +668,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
                         for (int y = 0; y < 2; ++y)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                f[r][y][h] = MODS ? 1.f : fmaxf(qs[r][y] * ks[h], 1e-37f);
+                                f[r][y][h] = MODS != 0 ? 1.f : fmaxf(qs[r][y] * ks[h], 1e-37f);
                                 const float top = fmaxf(s[r][h][y], s[r][h][2 + y]) * f[r][y][h];
                                 grows = grows || top > m[r][y] + kLazy || top + ev[h] > mo[r][y] + kLazy;
                             }
@@ -681,7 +691,6 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
                                 const float ref = mn == -INFINITY ? 0.f : mn, refo = mon == -INFINITY ? 0.f : mon;
                                 l[r][y] *= exp2_fast(m[r][y] - ref);
                                 ao[y] = exp2_fast(mo[r][y] - refo);
-                                shift[r][y] = mn == -INFINITY ? 0.f : exp2_fast(ref - refo);
                                 m[r][y] = mn;
                                 mo[r][y] = mon;
                             }
@@ -700,7 +709,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
                         scale_q[x] = scale_q[x + 1];
                     }
                     begin_tile(Shape::kDeep - 1, slot_k, bar_k);
-                    next_ord += kPagedWarps;
+                    next_ord += kWarps;
                     const int found = tile_of(next_ord);
                     const int found_a = page_at(found);
                     find_next(found, found_a, second_page(found, found_a));
@@ -708,6 +717,9 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
 #pragma unroll
                     for (int r = 0; r < NT; ++r) {
                         const float ref[2] = {m[r][0] == -INFINITY ? 0.f : m[r][0], m[r][1] == -INFINITY ? 0.f : m[r][1]};
+                        // 2^(m - mo), 0 for a row that has seen nothing
+                        const float shift[2] = {m[r][0] == -INFINITY ? 0.f : exp2_fast(m[r][0] - mo[r][0]),
+                                                m[r][1] == -INFINITY ? 0.f : exp2_fast(m[r][1] - mo[r][1])};
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -715,11 +727,11 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
                                 float e[2];
 #pragma unroll
                                 for (int y = 0; y < 2; ++y) {
-                                    e[y] = exp2_fast(MODS ? s[r][h][2 * z + y] - ref[y] : fmaf(s[r][h][2 * z + y], f[r][y][h], -ref[y]));
+                                    e[y] = exp2_fast(MODS != 0 ? s[r][h][2 * z + y] - ref[y] : fmaf(s[r][h][2 * z + y], f[r][y][h], -ref[y]));
                                     l[r][y] += e[y];
                                 }
                                 // P to 11 bits: an error of 2^-12 of each term, below the output's bf16 rounding
-                                pb[r][h][z] = transpose8x8(pack_half2(e[0] * (vs[h] * shift[r][0]), e[1] * (vs[h] * shift[r][1])));
+                                pb[r][h][z] = transpose8x8(pack_half2(e[0] * (vs[h] * shift[0]), e[1] * (vs[h] * shift[1])));
                             }
                     }
 
@@ -818,7 +830,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
             // ---- the four warps' parts of the segment become one
             __syncthreads();
             float* s_o = reinterpret_cast<float*>(smem);               // [warp][row][kPitch]
-            float* s_m = s_o + kPagedWarps * kRows * Shape::kPitch;    // [warp][row][4]
+            float* s_m = s_o + kWarps * kRows * Shape::kPitch;    // [warp][row][4]
 #pragma unroll
             for (int r = 0; r < NT; ++r)
 #pragma unroll
@@ -848,13 +860,13 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
                 hd[6] = static_cast<int32_t>(row0 >> 32);
                 hd[0] = 1 + static_cast<int32_t>((tiles - t1 + share - 1) / share);
             }
-            for (int x = tid; x < kRows * (D / 4); x += kPagedThreads) {
+            for (int x = tid; x < kRows * (D / 4); x += kBlockThreads) {
                 const int row = x / (D / 4), d = (x % (D / 4)) * 4;
                 if (row0 + row >= rows_all) continue;
-                float4 sm[kPagedWarps];
+                float4 sm[kWarps];
                 float mm = -INFINITY, mmo = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < kPagedWarps; ++w) {
+                for (int w = 0; w < kWarps; ++w) {
                     sm[w] = *reinterpret_cast<const float4*>(s_m + (w * kRows + row) * 4);
                     mm = fmaxf(mm, sm[w].x);
                     mmo = fmaxf(mmo, sm[w].y);
@@ -863,7 +875,7 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
                 float sum = 0.f;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int w = 0; w < kPagedWarps; ++w) {
+                for (int w = 0; w < kWarps; ++w) {
                     sum += sm[w].z * exp2_fast(sm[w].x - ref);
                     const float f = exp2_fast(sm[w].y - refo);
                     const float4 v = *reinterpret_cast<const float4*>(s_o + (w * kRows + row) * Shape::kPitch + d);
@@ -915,11 +927,11 @@ __global__ void __launch_bounds__(kPagedThreads, PagedShape<D, NT>::kBlocks)
 // blocks' first. A block has four rows: a warp for each, or, with many parts, all
 // warps on one row after another, each taking every fourth part.
 template <int D, int ROWS>
-__global__ void __launch_bounds__(kPagedThreads) paged_combine_kernel(const __grid_constant__ PagedParams p) {
+__global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(const __grid_constant__ PagedParams p) {
     constexpr float kLn2 = 0.6931471805599453f;
     constexpr int kPer = D / 32;  // columns of one lane
     constexpr int kFew = 16;
-    __shared__ float s_o[kPagedWarps][D];
+    __shared__ float s_o[kCombineWarps][D];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4* hd = reinterpret_cast<const int4*>(p.heads_of_parts + blockIdx.x * 8);
     const int4 h0 = hd[0];
@@ -929,8 +941,8 @@ __global__ void __launch_bounds__(kPagedThreads) paged_combine_kernel(const __gr
     const int64_t row0 = static_cast<int64_t>(static_cast<uint32_t>(h1.y)) | static_cast<int64_t>(h1.z) << 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool few = parts <= kFew;
-    for (int x = few ? warp : 0; x < kPagedWarps; x += few ? kPagedWarps : 1) {
-        const int in_tile = blockIdx.y * kPagedWarps + x;
+    for (int x = few ? warp : 0; x < kCombineWarps; x += few ? kCombineWarps : 1) {
+        const int in_tile = blockIdx.y * kCombineWarps + x;
         const int64_t row = row0 + in_tile;
         if (row >= static_cast<int64_t>(h0.w) * p.group) return;  // (uniform over the warps that share a row)
         auto slot_of = [&](int j) -> int64_t {
@@ -959,7 +971,7 @@ __global__ void __launch_bounds__(kPagedThreads) paged_combine_kernel(const __gr
 #pragma unroll
         for (int y = 0; y < kPer; ++y) acc[y] = 0.f;
 #pragma unroll 8
-        for (int j = few ? 0 : warp; j < parts; j += few ? 1 : kPagedWarps) {
+        for (int j = few ? 0 : warp; j < parts; j += few ? 1 : kCombineWarps) {
             const int64_t s = slot_of(j);
             const float f = exp2_fast(p.part_m[s * 4 + 1] - refo);
             const Pack<float, kPer> v = *reinterpret_cast<const Pack<float, kPer>*>(p.part_o + s * D + lane * kPer);
@@ -978,7 +990,7 @@ __global__ void __launch_bounds__(kPagedThreads) paged_combine_kernel(const __gr
             for (int y = 0; y < kPer; ++y) {
                 acc[y] = 0.f;
 #pragma unroll
-                for (int w = 0; w < kPagedWarps; ++w) acc[y] += s_o[w][lane * kPer + y];
+                for (int w = 0; w < kCombineWarps; ++w) acc[y] += s_o[w][lane * kPer + y];
             }
             if (warp != 0) continue;
         }

@@ -22,11 +22,12 @@ namespace {
 
 // Kernels whose shared memory size has been raised on a device.
 std::mutex g_set_mu;
-bool g_paged_set[64][24] = {{false}};
+bool g_paged_set[64][36] = {{false}};
 bool g_compact_set[64] = {false};
 
 constexpr int kMaxSeqs = 1 << 18;  // one bit each in the page planners' shared memory
-constexpr int kMaxPartBlocks = 1024;
+constexpr int kMaxPartBlocks = 160 * 3;        // of paged attention, three an SM
+constexpr int kMaxPartRows = 160 * 2 * 32;      // query rows of all its blocks: two of 32 or three of 16 an SM
 
 bsmt_status launched(const char* what) {
     const cudaError_t e = cudaGetLastError();
@@ -442,34 +443,34 @@ namespace {
 
 // O, the maxima and sums of two parts for each block, and the blocks' heads.
 int64_t paged_ws_bytes(int64_t D) {
-    return int64_t(kMaxPartBlocks) * 2 * 32 * (D + 4) * 4 + round256(int64_t(kMaxPartBlocks) * 32);
+    return int64_t(kMaxPartRows) * 2 * (D + 4) * 4 + round256(int64_t(kMaxPartBlocks) * 32);
 }
 
-template <int D, bool INT8, int NT, bool MODS>
+template <int D, bool INT8, int NT, int MODS>
 bsmt_status launch_paged(int dev, int nsm, bsmt::PagedParams p, const bsmt::MaskDnf& dnf, cudaStream_t s) {
     auto kern = bsmt::paged_attention_kernel<D, INT8, NT, MODS>;
     constexpr int smem = bsmt::PagedShape<D, NT>::kSmem;
     {
         std::lock_guard<std::mutex> lk(g_set_mu);
-        bool& set = g_paged_set[dev][(D == 128 ? 12 : 0) + (INT8 ? 6 : 0) + (NT / 2) * 2 + (MODS ? 1 : 0)];
+        bool& set = g_paged_set[dev][(D == 128 ? 18 : 0) + (INT8 ? 9 : 0) + (NT / 2) * 3 + MODS];
         if (!set) {
             const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
             if (e != cudaSuccess) return fail(BSMT_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
             set = true;
         }
     }
-    const int blocks = std::min(bsmt::PagedShape<D, NT>::kBlocks * nsm, kMaxPartBlocks);
+    const int blocks = std::min({bsmt::PagedShape<D, NT>::kBlocks * nsm, kMaxPartBlocks, kMaxPartRows / (8 * NT)});
     // the pools as rows of D codes; a copy takes the rows of a tile that lie in one page
     const int64_t rows = int64_t(p.c.layers) * p.c.pages * p.c.heads * p.c.page;
     CUtensorMap k_map, v_map;
     TRY(encode_rows(&k_map, p.c.k, rows, D, std::min(p.c.page, bsmt::kTileTokens)));
     TRY(encode_rows(&v_map, p.c.v, rows, D, std::min(p.c.page, bsmt::kTileTokens)));
-    kern<<<blocks, bsmt::kPagedThreads, smem, s>>>(p, dnf, k_map, v_map);
+    kern<<<blocks, 32 * bsmt::PagedShape<D, NT>::kWarps, smem, s>>>(p, dnf, k_map, v_map);
     TRY(launched("paged_attention"));
     // The combining kernel is set up while the first one runs, and waits for its end on the device.
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks, 2 * NT);
-    cfg.blockDim = dim3(bsmt::kPagedThreads);
+    cfg.blockDim = dim3(32 * bsmt::kCombineWarps);
     cfg.stream = s;
     cudaLaunchAttribute early;
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -483,15 +484,16 @@ bsmt_status launch_paged(int dev, int nsm, bsmt::PagedParams p, const bsmt::Mask
 }
 
 template <int D, bool INT8, int NT>
-bsmt_status launch_paged_mods(bool mods, int dev, int nsm, const bsmt::PagedParams& p, const bsmt::MaskDnf& dnf, cudaStream_t s) {
-    return mods ? launch_paged<D, INT8, NT, true>(dev, nsm, p, dnf, s) : launch_paged<D, INT8, NT, false>(dev, nsm, p, dnf, s);
+bsmt_status launch_paged_mods(int mods, int dev, int nsm, const bsmt::PagedParams& p, const bsmt::MaskDnf& dnf, cudaStream_t s) {
+    if (mods == 0) return launch_paged<D, INT8, NT, 0>(dev, nsm, p, dnf, s);
+    return mods == 1 ? launch_paged<D, INT8, NT, 1>(dev, nsm, p, dnf, s) : launch_paged<D, INT8, NT, 2>(dev, nsm, p, dnf, s);
 }
 
 template <int D, bool INT8>
-bsmt_status launch_paged_kind(int nt, bool mods, int dev, int nsm, const bsmt::PagedParams& p, const bsmt::MaskDnf& dnf, cudaStream_t s) {
+bsmt_status launch_paged_kind(int nt, int mods, int dev, int nsm, const bsmt::PagedParams& p, const bsmt::MaskDnf& dnf, cudaStream_t s) {
     if (nt == 1) return launch_paged_mods<D, INT8, 1>(mods, dev, nsm, p, dnf, s);
-    if (nt == 2) return launch_paged_mods<D, INT8, 2>(mods, dev, nsm, p, dnf, s);
-    return launch_paged_mods<D, INT8, 4>(mods, dev, nsm, p, dnf, s);
+    if (nt == 2 || D == 128) return launch_paged_mods<D, INT8, 2>(mods, dev, nsm, p, dnf, s);
+    return launch_paged_mods<D, INT8, D == 64 ? 4 : 2>(mods, dev, nsm, p, dnf, s);
 }
 
 }  // namespace
@@ -545,8 +547,8 @@ extern "C" bsmt_status bsmt_paged_attention(const void* q, int64_t T, int64_t Hq
     p.out = static_cast<__nv_bfloat16*>(out);
     p.lse = lse;
     p.part_o = static_cast<float*>(workspace);
-    p.part_m = p.part_o + int64_t(kMaxPartBlocks) * 2 * 32 * p.c.dim;
-    p.heads_of_parts = reinterpret_cast<int32_t*>(p.part_m + int64_t(kMaxPartBlocks) * 2 * 32 * 4);
+    p.part_m = p.part_o + int64_t(kMaxPartRows) * 2 * p.c.dim;
+    p.heads_of_parts = reinterpret_cast<int32_t*>(p.part_m + int64_t(kMaxPartRows) * 2 * 4);
     p.slopes = sa.slopes;
     p.T = T;
     p.n = static_cast<int32_t>(n);
@@ -558,14 +560,15 @@ extern "C" bsmt_status bsmt_paged_attention(const void* q, int64_t T, int64_t Hq
     p.cap = sa.cap;
     // the modes of the score program: none, soft-cap, ALiBi, soft-cap then ALiBi, ALiBi then soft-cap
     p.softcap = sa.mode == 1 || sa.mode == 3 || sa.mode == 4;
-    p.alibi = sa.mode == 2 || sa.mode == 3 || sa.mode == 4;
     p.alibi_first = sa.mode == 4;
     p.alibi_h0 = sa.alibi_h0;
     p.alibi_heads = sa.alibi_heads;
-    // Row tiles of 8, 16 or 32: the smallest that holds an average sequence's rows, so that its keys are read once.
+    // Row tiles of 8 or 16, or, at D = 64, 32: the smallest that holds an average sequence's rows, so that its keys are
+    // read once. (32 rows of 24 sequences up to 64k: 16 a tile 433 us at D = 64, 588 at D = 128, where O spills with 32;
+    // 32 a tile 392 and 668.)
     const int64_t rows = (T * p.group + std::max<int64_t>(n, 1) - 1) / std::max<int64_t>(n, 1);
-    const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
-    const bool mods = sa.mode != 0;
+    const int nt = rows <= 8 ? 1 : rows <= 16 || p.c.dim == 128 ? 2 : 4;
+    const int mods = sa.mode <= 1 ? sa.mode : 2;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     bsmt_status st;
     if (p.c.dim == 128)
