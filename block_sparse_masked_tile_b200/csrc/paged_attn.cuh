@@ -150,7 +150,7 @@ __device__ __forceinline__ uint32_t flip(uint32_t w) {
 
 // The tiles that some query in [q_lo, q_hi] of a sequence of `len` tokens sees:
 // up to kMaxTerms disjoint runs, ascending. Returns the number of tiles.
-__device__ __noinline__ int seen_tiles(const MaskDnf& dnf, int64_t q_lo, int64_t q_hi, int64_t len, int* first,
+__device__ __forceinline__ int seen_tiles(const MaskDnf& dnf, int64_t q_lo, int64_t q_hi, int64_t len, int* first,
                                           int* last, int* runs) {
     int n = 0, total = 0;
     for (int t = 0; t < dnf.n_terms; ++t) {
@@ -192,7 +192,7 @@ struct PagedSeq {
     int count;          // queries
 };
 
-__device__ __noinline__ PagedSeq paged_seq(const PagedParams& p, int i) {
+__device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int i) {
     PagedSeq s;
     s.slot = __ldg(p.seqs + i);
     int64_t q0 = i, q1 = i + 1;
@@ -267,6 +267,10 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
     const uint32_t bars = shared_addr(s_bars) + warp * 2 * Shape::kDeep * 8;
     if (lane < 2 * Shape::kDeep) bar_init(bars + lane * 8);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (tid == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&k_map)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&v_map)) : "memory");
+    }
 
     // ---- this block's share of all tiles
     const int per_thread = (p.n + kBlockThreads - 1) / kBlockThreads;
