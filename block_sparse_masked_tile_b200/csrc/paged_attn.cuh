@@ -220,11 +220,18 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int i) {
     return s;
 }
 
+// A sequence and the tiles that its queries see.
+struct PagedPlan {
+    PagedSeq s;
+    int tiles, runs;
+    int first[kMaxTerms], last[kMaxTerms];
+};
+
 // What the blocks need of the sequence that they work on.
 struct PagedSeqShared {
     PagedSeq s;
-    int64_t weight;  // tiles of all its units
-    int tiles, row_tiles, runs;
+    int64_t weight;  // of all its units
+    int tiles;
     int first[kMaxTerms], last[kMaxTerms];          // runs of seen tiles
     int32_t clean_lo[kMaxTerms], clean_hi[kMaxTerms];  // keys that every query sees, for each term
 };
@@ -275,27 +282,30 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
     // ---- this block's share of all tiles
     const int per_thread = (p.n + kBlockThreads - 1) / kBlockThreads;
     const int i_lo = min(p.n, tid * per_thread), i_hi = min(p.n, i_lo + per_thread);
-    auto describe = [&](const PagedSeq& s) {  // what the whole block needs of a sequence
-        s_seq.s = s;
-        s_seq.tiles = seen_tiles(dnf, s.len - s.count, s.len - 1, s.len, s_seq.first, s_seq.last, &s_seq.runs);
-        s_seq.weight = paged_weight<kRows>(p, s, s_seq.tiles);
+    auto plan = [&](int i, PagedPlan& d) {  // returns the sequence's weight
+        d.s = paged_seq(p, i);
+        d.tiles = seen_tiles(dnf, d.s.len - d.s.count, d.s.len - 1, d.s.len, d.first, d.last, &d.runs);
+        return paged_weight<kRows>(p, d.s, d.tiles);
+    };
+    auto describe = [&](const PagedPlan& d) {  // for the whole block
+        s_seq.s = d.s;
+        s_seq.tiles = d.tiles;
+        s_seq.weight = paged_weight<kRows>(p, d.s, d.tiles);
+        for (int x = 0; x < d.runs; ++x) {
+            s_seq.first[x] = d.first[x];
+            s_seq.last[x] = d.last[x];
+        }
         for (int x = 0; x < dnf.n_terms; ++x) {
             int64_t lo, hi, unused;  // (both within [-len, len])
-            term_interval(dnf, x, s.len - 1, 0, s.len - 1, 0, 0, lo, unused);
-            term_interval(dnf, x, s.len - s.count, 0, s.len - 1, 0, 0, unused, hi);
+            term_interval(dnf, x, d.s.len - 1, 0, d.s.len - 1, 0, 0, lo, unused);
+            term_interval(dnf, x, d.s.len - d.s.count, 0, d.s.len - 1, 0, 0, unused, hi);
             s_seq.clean_lo[x] = static_cast<int32_t>(min(lo, static_cast<int64_t>(INT32_MAX)));
             s_seq.clean_hi[x] = static_cast<int32_t>(max(hi, static_cast<int64_t>(-1)));
         }
     };
     long long mine = 0;
-    PagedSeq own;  // the thread's sequence, where there is one for each thread at most
-    own.count = 0;
-    for (int i = i_lo; i < i_hi; ++i) {
-        own = paged_seq(p, i);
-        int first[kMaxTerms], last[kMaxTerms], runs;
-        const int tiles = seen_tiles(dnf, own.len - own.count, own.len - 1, own.len, first, last, &runs);
-        mine += paged_weight<kRows>(p, own, tiles);
-    }
+    PagedPlan own;  // the thread's sequence, where there is one for each thread at most
+    for (int i = i_lo; i < i_hi; ++i) mine += plan(i, own);
     long long incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -320,10 +330,7 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
         int i = i_lo;
         if (per_thread > 1) {
             for (; i < i_hi; ++i) {
-                own = paged_seq(p, i);
-                int first[kMaxTerms], last[kMaxTerms], runs;
-                const int tiles = seen_tiles(dnf, own.len - own.count, own.len - 1, own.len, first, last, &runs);
-                const long long w = paged_weight<kRows>(p, own, tiles);
+                const long long w = plan(i, own);
                 if (off < w) break;
                 off -= w;
             }
@@ -449,6 +456,7 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
                 next_a = a;
                 next_b = b;
             };
+            uint4 q_raw[NT][kChunks][2];
             {
                 int first_tok[Shape::kDeep + 1], first_a[Shape::kDeep + 1], first_b[Shape::kDeep + 1];  // (read together)
 #pragma unroll
@@ -456,6 +464,21 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
                     first_tok[x] = tile_of(next_ord + x * kWarps);
                     first_a[x] = page_at(first_tok[x]);
                     first_b[x] = second_page(first_tok[x], first_a[x]);
+                }
+                // q's rows g of each 8, read meanwhile
+#pragma unroll
+                for (int r = 0; r < NT; ++r) {
+                    const int row = 8 * r + g;
+                    const bool valid = row0 + row < rows_all;
+                    const int up_q = static_cast<int>(static_cast<uint32_t>(in_group + row) / static_cast<uint32_t>(p.group));
+                    const int64_t qi = valid ? qi0 + up_q : 0;
+                    const int hq = head * p.group + (valid ? in_group + row - up_q * p.group : 0);
+                    const uint4* src = reinterpret_cast<const uint4*>(p.q + ((s_seq.s.q0 + qi) * p.Hq + hq) * D + 16 * t);
+#pragma unroll
+                    for (int x = 0; x < kChunks; ++x) {
+                        q_raw[r][x][0] = valid ? __ldg(src + 8 * x) : make_uint4(0, 0, 0, 0);
+                        q_raw[r][x][1] = valid ? __ldg(src + 8 * x + 1) : make_uint4(0, 0, 0, 0);
+                    }
                 }
                 uint32_t slot = slot_k, bar = bar_k;
 #pragma unroll
@@ -472,7 +495,7 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
                 next_ord += Shape::kDeep * kWarps;
             }
 
-            // ---- q: row g of each 8, in halves; what the softmax needs of rows 2 t and 2 t + 1
+            // ---- q in halves; what the softmax needs of rows 2 t and 2 t + 1
             uint32_t qf[kQShared ? 1 : NT][kSteps][2];
             float qs[NT][2], slope[MODS == 2 ? NT : 1][2];
             auto pos_of = [&](int r, int y) {  // position of the query of row 8 r + 2 t + y
@@ -483,17 +506,10 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
             const uint32_t q_smem = shared_addr(smem) + Shape::kQ + lane * 8;
 #pragma unroll
             for (int r = 0; r < NT; ++r) {
-                const int row = 8 * r + g;
-                const bool valid = row0 + row < rows_all;
-                const int up_q = static_cast<int>(static_cast<uint32_t>(in_group + row) / static_cast<uint32_t>(p.group));
-                const int64_t qi = valid ? qi0 + up_q : 0;
-                const int hq = head * p.group + (valid ? in_group + row - up_q * p.group : 0);
                 uint32_t w[kChunks][8];
-                const uint4* src = reinterpret_cast<const uint4*>(p.q + ((s_seq.s.q0 + qi) * p.Hq + hq) * D + 16 * t);
 #pragma unroll
                 for (int x = 0; x < kChunks; ++x) {
-                    const uint4 a = valid ? __ldg(src + 8 * x) : make_uint4(0, 0, 0, 0);
-                    const uint4 b = valid ? __ldg(src + 8 * x + 1) : make_uint4(0, 0, 0, 0);
+                    const uint4 a = q_raw[r][x][0], b = q_raw[r][x][1];
                     w[x][0] = a.x, w[x][1] = a.y, w[x][2] = a.z, w[x][3] = a.w;
                     w[x][4] = b.x, w[x][5] = b.y, w[x][6] = b.z, w[x][7] = b.w;
                 }
@@ -919,7 +935,8 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
             if (per_thread == 1) {
                 if (tid == i) describe(own);
             } else if (tid == 0) {
-                describe(paged_seq(p, i));
+                plan(i, own);
+                describe(own);
             }
             __syncthreads();
         } while (s_seq.weight == 0);
