@@ -267,7 +267,7 @@ extern "C" bsmt_status bsmt_cache_write(const bsmt_kv_cache* cache, int32_t laye
     p.layer = layer;
     p.items = cu_seqlens == nullptr ? n : (T >> p.c.page_shift) + 2 * n;
     // A warp for each page, head and tensor in calls of at most four tokens a sequence on average, else a block for each
-    // page and some of the heads: few enough that there are 8 blocks an SM.
+    // page and some of the heads: few enough that there are 16 blocks an SM.
     const bool few = T <= 4 * n;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (few) {
@@ -279,7 +279,7 @@ extern "C" bsmt_status bsmt_cache_write(const bsmt_kv_cache* cache, int32_t laye
             bsmt::cache_write_rows_kernel<false><<<static_cast<unsigned>(blocks), 256, 0, s>>>(p);
     } else {
         const int64_t heads = 2 * int64_t(p.c.heads);
-        p.share = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(heads, p.items * heads / (8 * int64_t(nsm)))));
+        p.share = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(heads, p.items * heads / (16 * int64_t(nsm)))));
         const int64_t blocks = p.items * ((heads + p.share - 1) / p.share);
         if (blocks > 0x7FFFFFFF) return fail(BSMT_ERR_UNSUPPORTED, "cache_write: grid too large");
         const unsigned grid = static_cast<unsigned>(blocks);
