@@ -113,6 +113,15 @@ __device__ __forceinline__ float rcp_fast(float x) {
     return y;
 }
 
+// tanh(u) = 1 - 2 / (exp(2 u) + 1), off by 2^-23 or so; for small u, where that would be much of the value, the
+// first terms of its series (the next is below 2^-26 of it).
+__device__ __forceinline__ float tanh_fast(float u) {
+    const float q = u * u;
+    const float series = u * fmaf(q, fmaf(q, fmaf(q, fmaf(q, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), 1.f);
+    const float direct = 1.f - 2.f * rcp_fast(exp2_fast(u * 2.885390082f) + 1.f);
+    return q < 0.0625f ? series : direct;
+}
+
 // A word's codes 0, 1 as the halves lo and codes 2, 3 as hi. The int8 codes come
 // with their top bit flipped (u = code + 128): the half 0x6400 | u is 1024 + u.
 template <bool INT8>
@@ -640,16 +649,19 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
                             }
                     }
                     if (MODS == 1) {
-                        // cap * tanh(z / cap), tanh(u) = 1 - 2 / (exp(2 u) + 1), in units of log2
+                        // cap * tanh(z / cap), in units of log2. Up to a cap of 64 the exponential's form alone: its error
+                        // is cap * 2^-23, below a score's own. Beyond, a score may be small beside the cap.
                         const float cap2 = p.cap * kLog2e;
+                        const bool direct = p.cap <= 64.f;
 #pragma unroll
                         for (int r = 0; r < NT; ++r)
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
-                                    const float u = exp2_fast(s[r][h][e] * (qs[r][e & 1] * ks[h] * (2.f * kLog2e / p.cap)));
-                                    s[r][h][e] = fmaf(-2.f * cap2, rcp_fast(u + 1.f), cap2);
+                                    const float z = s[r][h][e] * (qs[r][e & 1] * ks[h]);
+                                    s[r][h][e] = direct ? fmaf(-2.f * cap2, rcp_fast(exp2_fast(z * (2.f * kLog2e / p.cap)) + 1.f), cap2)
+                                                        : cap2 * tanh_fast(z / p.cap);
                                 }
                     } else if (MODS == 2) {
                         const int rel = tok - pos[0][0] + tok_g;
@@ -663,7 +675,7 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
                                     float z = s[r][h][e] * (qs[r][y] * ks[h]);
                                     const float bias = slope[r][y] * static_cast<float>(rel + 16 * h + 8 * (e >> 1) - (pos[r][y] - pos[0][0]));
                                     if (p.alibi_first) z += bias;
-                                    if (p.softcap) z = p.cap * (1.f - 2.f * rcp_fast(exp2_fast(z * (2.f * kLog2e / p.cap)) + 1.f));
+                                    if (p.softcap) z = p.cap * tanh_fast(z / p.cap);
                                     if (!p.alibi_first) z += bias;
                                     s[r][h][e] = z * kLog2e;
                                 }

@@ -226,7 +226,8 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, spe
     strides (views of one fused projection are fine). ``positions``: int32
     [num_axes, T], [num_axes, B, T] for 4-D tensors, or [T] with one axis; any
     int32 value. Returns the turned (q, k), contiguous. Differentiable in q and
-    k."""
+    k. (As with any torch operation, a step with its backward pass is captured
+    into a CUDA graph while no eager graph of the same leaves is alive.)"""
     tensors = _rotary_args(q, k, positions, spec)
     if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
         outs = list(_RotaryFn.apply(positions, spec, False, *tensors))
@@ -361,7 +362,8 @@ def cache_write(cache: PagedCache, seqs: torch.Tensor, starts: torch.Tensor, k: 
     """Quantises k, v (bf16 [T, Hkv, D]; the innermost dimension contiguous, the
     other strides multiples of 8) into the pages of sequences seqs from positions
     ``starts`` on, as cache_extend returned them. ``cu_seqlens`` (int32
-    [n + 1]): the sequences' tokens in the pack; None: one token each."""
+    [n + 1]): the sequences' tokens in the pack; None: one token each. A
+    sequence may be listed once."""
     c, dev = _on_gpu(cache)
     n = seqs.numel()
     _, _, heads, _, dim = cache.k.shape

@@ -141,8 +141,9 @@ bsmt_status bsmt_cache_extend(const bsmt_kv_cache* cache, const int32_t* seqs, c
  * part in the scale. An entry with seqs[i] or starts[i] = -1 is passed over.
  * Positions past the sequence's length and pages out of range are not written
  * (BSMT_ERR_DEVICE_BOUNDS), pages held by another sequence too or by none
- * are not written (BSMT_ERR_DEVICE_PRECONDITION). The positions of one call
- * must not repeat. */
+ * are not written (BSMT_ERR_DEVICE_PRECONDITION). A sequence may be listed
+ * once in a call: two entries that meet in a page would race for its scale
+ * (bsmt_cache_extend refuses such a list). */
 bsmt_status bsmt_cache_write(const bsmt_kv_cache* cache, int32_t layer, const int32_t* seqs, const int32_t* starts,
                              int64_t n, const int32_t* cu_seqlens, const void* k, const void* v, int64_t T,
                              const int64_t k_strides[2], const int64_t v_strides[2], void* stream);
@@ -160,7 +161,8 @@ bsmt_status bsmt_cache_gather(const bsmt_kv_cache* cache, int32_t layer, const i
  * pages are shared (their counts grow); a partial last page is copied, in
  * every layer, to a page taken for the child. A parent may be listed many
  * times, a child once. All or nothing as bsmt_cache_extend; a child that is
- * not empty or listed twice is BSMT_ERR_DEVICE_PRECONDITION. */
+ * not empty or listed twice is BSMT_ERR_DEVICE_PRECONDITION. (A number out of
+ * range among a parent's full pages is copied as it stands and reported.) */
 bsmt_status bsmt_cache_fork(const bsmt_kv_cache* cache, const int32_t* src, const int32_t* dst, int64_t n,
                             void* workspace, int64_t workspace_bytes, void* stream);
 

@@ -5,6 +5,7 @@ import torch
 
 import block_sparse_masked_tile_b200 as bsmt
 import workloads
+from oracle import serving as osv
 from tests.serving_helpers import Both, ints, queries
 
 pytestmark = pytest.mark.gpu
@@ -73,6 +74,17 @@ def test_score_mods(mods, dim, code, count):
     b.attend(queries(3 * count, 8, dim), [2, 1, 0], [count] * 3, STREAM, mods, scale=0.3)
 
 
+@pytest.mark.parametrize("cap", [0.25, 64.0, 65.0, 1e4, 1e30])
+@pytest.mark.parametrize("also", [(), (("alibi", None),)])
+def test_soft_caps_of_any_size(cap, also):
+    # far above the scores a cap changes nothing; far below, every score is its sign times the cap
+    b = filled([150, 33], 2, 64, 32, "e4m3")
+    q = queries(4, 4, 64)
+    out, lse = b.attend(q, [0, 1], [2, 2], ("causal",), (("softcap", cap),) + also)
+    if cap == 1e30:
+        b.close(out, lse, *osv.paged_attention(q.double().numpy(), b.ref, [0, 1], [0, 2, 4], ("causal",), also), q)
+
+
 def test_padded_batches_and_empty_sequences():
     b = filled([40, 0, 17], 2, 128, 16, "e4m3")
     q = queries(10, 4, 128)
@@ -115,7 +127,6 @@ def test_scales_far_apart():
         b.write(0, [0], starts, b.values(16) * 2.0 ** (e % 7 - 3), b.values(16) * 2.0 ** e, [16])
     b.equal()
     q = queries(1, 4, 64)
-    from oracle import serving as osv
     for tree in (None, ("window", 17), ("and", ("sink", 16), ("causal",))):
         mask = None if tree is None else bsmt.mask_from_tree(tree)
         out, lse = bsmt.paged_attention(q.cuda(), b.dev, ints([0]), None, mask, enable_gqa=True)
@@ -144,7 +155,6 @@ def test_large_small_and_non_finite_queries():
     out, lse = bsmt.paged_attention(q.cuda(), b.dev, seqs, cu, bsmt.causal(), None, 2.0 ** -60, True)
     bsmt.check_device_status()
     assert torch.isnan(out[2, 0]).all() and torch.isnan(lse[0, 2]) and torch.isnan(out[3, 1]).all()
-    from oracle import serving as osv
     with np.errstate(invalid="ignore"):
         want, want_lse = osv.paged_attention(q.double().numpy(), b.ref, [0], [0, 6], ("causal",), (), 2.0 ** -60)
     fine = [0, 1, 4, 5]
