@@ -144,6 +144,34 @@ void launch_rotary(const bsmt::RotaryParams& p, int vec, bool interleaved, dim3 
 }
 }  // namespace
 
+extern "C" bsmt_status bsmt_rotary_sections(int32_t head_dim, const int32_t* sections, int32_t num_sections, double base,
+                                            int32_t per_axis, int32_t interleaved, bsmt_rotary_spec* out) {
+    if (out == nullptr || (num_sections > 0 && sections == nullptr))
+        return fail(BSMT_ERR_INVALID_ARGUMENT, "rotary: sections and out must be non-NULL");
+    if (num_sections < 1 || num_sections > 127) return fail(BSMT_ERR_INVALID_ARGUMENT, "rotary: %d axes", num_sections);
+    if (!(base > 0) || !std::isfinite(base)) return fail(BSMT_ERR_INVALID_ARGUMENT, "rotary: base must be finite and > 0");
+    int64_t pairs = 0;
+    for (int32_t a = 0; a < num_sections; ++a) {
+        if (sections[a] < 0) return fail(BSMT_ERR_INVALID_ARGUMENT, "rotary: sections[%d] is negative", a);
+        pairs += sections[a];
+    }
+    if (pairs < 1 || pairs > BSMT_MAX_ROTARY_PAIRS || head_dim < 2 * pairs)
+        return fail(BSMT_ERR_INVALID_ARGUMENT, "rotary: %lld pairs in a head of %d (1 to %d pairs)", static_cast<long long>(pairs), head_dim,
+                    BSMT_MAX_ROTARY_PAIRS);
+    std::memset(out, 0, sizeof(*out));
+    out->head_dim = head_dim;
+    out->num_pairs = static_cast<int32_t>(pairs);
+    out->num_axes = num_sections;
+    out->interleaved = interleaved != 0;
+    int32_t i = 0;
+    for (int32_t a = 0; a < num_sections; ++a)
+        for (int32_t j = 0; j < sections[a]; ++j, ++i) {
+            out->inv_freq[i] = per_axis ? std::pow(base, -static_cast<double>(j) / sections[a]) : std::pow(base, -static_cast<double>(i) / pairs);
+            out->axis[i] = static_cast<int8_t>(a);
+        }
+    return ok();
+}
+
 extern "C" bsmt_status bsmt_rotary(const bsmt_rotary_spec* spec, int32_t dtype, int64_t B, int64_t T,
                                    const int32_t* positions, const int64_t position_strides[3], int32_t inverse,
                                    const bsmt_rotary_tensor* tensors, int32_t num_tensors, void* stream) {

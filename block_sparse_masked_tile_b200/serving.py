@@ -58,6 +58,8 @@ class _KvCache(ctypes.Structure):
 def _declare() -> None:
     cache, strides = ctypes.POINTER(_KvCache), ctypes.POINTER(_i64)
     for name, args in {
+        "bsmt_rotary_sections": [_i32, ctypes.POINTER(_i32), _i32, ctypes.c_double, _i32, _i32,
+                                 ctypes.POINTER(_RotarySpecC)],
         "bsmt_rotary": [ctypes.POINTER(_RotarySpecC), _i32, _i64, _i64, _vp, strides, _i32,
                         ctypes.POINTER(_RotaryTensor), _i32, _vp],
         "bsmt_cache_workspace_bytes": [cache, _i64, strides],
@@ -131,14 +133,16 @@ def rotary_spec(head_dim: int, sections: Sequence[int] | None = None, base: floa
 
     inv_freq is base^(-i / pairs) over all pairs in one ladder, or with
     ``per_axis`` base^(-j / sections[a]) over each axis's own."""
-    sections = [int(head_dim) // 2] if sections is None else [int(s) for s in sections]
-    if any(s < 0 for s in sections) or sum(sections) < 1:
-        raise ValueError(f"sections {sections}: pair counts must not be negative, and some pair must turn")
-    base = float(base)
-    axis = [a for a, s in enumerate(sections) for _ in range(s)]
-    ladders = [s for s in sections if s] if per_axis else [len(axis)]
-    freq = [base ** (-j / n) for n in ladders for j in range(n)]
-    return RotarySpec(int(head_dim), tuple(freq), tuple(axis), len(sections), bool(interleaved))
+    sections = [int(head_dim) // 2] if sections is None else list(sections)
+    c = _RotarySpecC()
+    _check(_lib.bsmt_rotary_sections(head_dim, (_i32 * len(sections))(*sections), len(sections), base, bool(per_axis),
+                                     bool(interleaved), _byref(c)))
+    spec = object.__new__(RotarySpec)  # (the library has checked it)
+    n = c.num_pairs
+    for name, value in (("head_dim", c.head_dim), ("inv_freq", tuple(c.inv_freq[:n])), ("axis", tuple(c.axis[:n])),
+                        ("num_axes", c.num_axes), ("interleaved", bool(c.interleaved)), ("_c", c)):
+        object.__setattr__(spec, name, value)
+    return spec
 
 
 def _heads_tokens(t: torch.Tensor) -> tuple:

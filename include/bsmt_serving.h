@@ -38,6 +38,12 @@ typedef struct bsmt_rotary_spec {
     int8_t axis[BSMT_MAX_ROTARY_PAIRS];      /* 0 .. num_axes - 1 */
 } bsmt_rotary_spec;
 
+/* Fills a spec with sections[a] >= 0 consecutive pairs for axis a. inv_freq is
+ * base^(-i / pairs) over all pairs in one ladder, or with per_axis != 0
+ * base^(-j / sections[a]) over each axis's own. base > 0. Host-only. */
+bsmt_status bsmt_rotary_sections(int32_t head_dim, const int32_t* sections, int32_t num_sections, double base,
+                                 int32_t per_axis, int32_t interleaved, bsmt_rotary_spec* out);
+
 /* One tensor [B, heads, T, head_dim] in device memory, its innermost
  * dimension contiguous, the other strides any (in elements; batch, head,
  * token). `out` may be `in` with the same strides, and must not overlap it

@@ -33,7 +33,7 @@ def test_header_declares_what_the_binding_calls():
     names = sorted(set(re.findall(r"^bsmt_status\s+(bsmt_\w+)\s*\(", text, re.M)))
     assert names == ["bsmt_cache_compact", "bsmt_cache_extend", "bsmt_cache_fork", "bsmt_cache_free", "bsmt_cache_gather",
                      "bsmt_cache_workspace_bytes", "bsmt_cache_write", "bsmt_paged_attention",
-                     "bsmt_paged_attention_workspace_bytes", "bsmt_rotary"]
+                     "bsmt_paged_attention_workspace_bytes", "bsmt_rotary", "bsmt_rotary_sections"]
     for n in names:
         assert hasattr(_lib, n), n
 
@@ -164,6 +164,13 @@ def test_rotary_spec():
     for args in ((64, [33]), (64, []), (64, [-1, 4]), (64, [0, 0])):
         with pytest.raises(ValueError):
             bsmt.rotary_spec(*args)
+    for base in (0.0, -1.0, math.inf, math.nan):
+        with pytest.raises(ValueError, match="base"):
+            bsmt.rotary_spec(64, base=base)
+    # the same spec, pair by pair
+    s = bsmt.rotary_spec(80, [10, 0, 7], base=500.0, interleaved=True)
+    t = bsmt.RotarySpec(80, tuple(500.0 ** (-i / 17) for i in range(17)), (0,) * 10 + (2,) * 7, 3, True)
+    assert s == t and bytes(s._c) == bytes(t._c)
     with pytest.raises(ValueError, match="axes"):
         bsmt.RotarySpec(64, (1.0, 0.5), (0,))
     with pytest.raises(ValueError, match="axis"):
