@@ -420,14 +420,17 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
             const int in_group = static_cast<int>(row0 - qi0 * p.group);  // row0 = qi0 * group + in_group
 
             // ---- pipeline over this warp's tiles
-            int run = 0, run_base = 0;  // the run that the next tile to load lies in, and the tiles before it
+            const int stop = min(t1, seen);
+            int run = -1, run_end = 0, run_off = 0;  // the run that the next tile to load lies in: its last ordinal + 1, and
+                                                     // its first tile less its first ordinal
             auto tile_of = [&](int ord) -> int {  // first token of the unit's tile `ord`; -1: none
-                if (ord >= t1 || ord >= seen) return -1;
-                while (ord - run_base > s_seq.last[run] - s_seq.first[run]) {
-                    run_base += s_seq.last[run] - s_seq.first[run] + 1;
+                if (ord >= stop) return -1;
+                while (ord >= run_end) {
                     ++run;
+                    run_off = s_seq.first[run] - run_end;
+                    run_end += s_seq.last[run] - s_seq.first[run] + 1;
                 }
-                return (s_seq.first[run] + ord - run_base) * kTileTokens;
+                return (ord + run_off) * kTileTokens;
             };
             auto page_at = [&](int tok) -> int {  // page of a token; -1: behind the sequence
                 if (tok < 0 || tok >= len) return -1;
@@ -571,6 +574,7 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
             }
             if (kQShared) __syncthreads();
 
+            const int clean_lo = s_seq.clean_lo[0], clean_hi = s_seq.clean_hi[0];
             float o[NT][kOut][4];
             float m[NT][2], mo[NT][2], l[NT][2];
 #pragma unroll
@@ -630,8 +634,8 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
                     const float ev[2] = {__log2f(fmaxf(vs[0], 0x1p-126f)), __log2f(fmaxf(vs[1], 0x1p-126f))};
 
                     // which keys the rows see
-                    bool clean = false;
-                    for (int x = 0; x < dnf.n_terms; ++x)
+                    bool clean = clean_lo <= tok && tok + kTileTokens - 1 <= clean_hi;
+                    for (int x = 1; x < dnf.n_terms; ++x)
                         clean = clean || (s_seq.clean_lo[x] <= tok && tok + kTileTokens - 1 <= s_seq.clean_hi[x]);
                     uint32_t bits[NT][2];
                     if (!clean) {
@@ -651,18 +655,22 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
                     if (MODS == 1) {
                         // cap * tanh(z / cap), in units of log2. Up to a cap of 64 the exponential's form alone: its error
                         // is cap * 2^-23, below a score's own. Beyond, a score may be small beside the cap.
-                        const float cap2 = p.cap * kLog2e;
-                        const bool direct = p.cap <= 64.f;
+                        const float cap2 = p.cap * kLog2e, inv = 1.f / p.cap;
 #pragma unroll
                         for (int r = 0; r < NT; ++r)
 #pragma unroll
-                            for (int h = 0; h < 2; ++h)
+                            for (int h = 0; h < 2; ++h) {
+                                const float u[2] = {qs[r][0] * ks[h] * inv, qs[r][1] * ks[h] * inv};
+                                if (p.cap <= 64.f) {
+                                    const float w[2] = {u[0] * (2.f * kLog2e), u[1] * (2.f * kLog2e)};
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const float z = s[r][h][e] * (qs[r][e & 1] * ks[h]);
-                                    s[r][h][e] = direct ? fmaf(-2.f * cap2, rcp_fast(exp2_fast(z * (2.f * kLog2e / p.cap)) + 1.f), cap2)
-                                                        : cap2 * tanh_fast(z / p.cap);
+                                    for (int e = 0; e < 4; ++e)
+                                        s[r][h][e] = fmaf(-2.f * cap2, rcp_fast(exp2_fast(s[r][h][e] * w[e & 1]) + 1.f), cap2);
+                                } else {
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) s[r][h][e] = cap2 * tanh_fast(s[r][h][e] * u[e & 1]);
                                 }
+                            }
                     } else if (MODS == 2) {
                         const int rel = tok - pos[0][0] + tok_g;
 #pragma unroll
