@@ -200,22 +200,23 @@ class _RotaryFn(torch.autograd.Function):
 def _rotary_args(q, k, positions, spec) -> list:
     tensors = [q] if k is None else [q, k]
     for name, t in zip("qk", tensors):
+        shape = t.shape
         if t.dtype not in _ROTARY_DTYPES:
             raise ValueError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
-        if t.dim() not in (3, 4):
+        if len(shape) != 3 and len(shape) != 4:
             raise ValueError(f"{name} must be [T, H, D] or [B, H, T, D]")
-        if t.shape[-1] != spec.head_dim:
-            raise ValueError(f"{name} has head dim {t.shape[-1]}, the spec {spec.head_dim}")
-        if t.stride(-1) != 1 and t.shape[-1] > 1:
+        if shape[-1] != spec.head_dim:
+            raise ValueError(f"{name} has head dim {shape[-1]}, the spec {spec.head_dim}")
+        if t.stride(-1) != 1 and shape[-1] > 1:
             raise ValueError(f"{name}'s innermost dimension must be contiguous")
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
     B, _, T, _ = _heads_tokens(q)
     if k is not None:
         Bk, _, Tk, _ = _heads_tokens(k)
-        if k.dtype != q.dtype or k.device != q.device or k.dim() != q.dim() or Bk != B or Tk != T:
+        if k.dtype is not q.dtype or k.get_device() != q.get_device() or k.dim() != q.dim() or Bk != B or Tk != T:
             raise ValueError(f"q and k must share type, device, batch and tokens: q {tuple(q.shape)}, k {tuple(k.shape)}")
-    if positions.dtype != torch.int32 or positions.device != q.device:
+    if positions.dtype is not torch.int32 or positions.get_device() != q.get_device():
         raise ValueError(f"positions must be int32 on {q.device} (got {positions.dtype} on {positions.device})")
     shape, axes = tuple(positions.shape), spec.num_axes
     if shape != (axes, T) and not (shape == (T,) and axes == 1) and not (shape == (axes, B, T) and q.dim() == 4):
@@ -266,7 +267,7 @@ class PagedCache:
     ref_counts: torch.Tensor
 
     def __post_init__(self):
-        k, v, table, dev = self.k, self.v, self.page_table, self.k.device
+        k, v, table, at = self.k, self.v, self.page_table, self.k.get_device()  # (-1: the host)
         if k.dim() != 5 or k.dtype not in _CACHE_DTYPES:
             raise ValueError("cache codes must be float8_e4m3fn or int8 [layers, pages, Hkv, page_size, D]")
         if table.dim() != 2:
@@ -278,8 +279,8 @@ class PagedCache:
                                      ("k_scale", self.k_scale, f32, shape[:3]), ("v_scale", self.v_scale, f32, shape[:3]),
                                      ("page_table", table, i32, table.shape), ("seq_lens", self.seq_lens, i32, (seqs,)),
                                      ("ref_counts", self.ref_counts, i32, (pages,))):
-            if t.dtype != dtype or t.shape != want or t.device != dev or not t.is_contiguous():
-                raise ValueError(f"cache {name} must be contiguous {dtype} {tuple(want)} on {dev} "
+            if t.dtype is not dtype or t.shape != want or t.get_device() != at or not t.is_contiguous():
+                raise ValueError(f"cache {name} must be contiguous {dtype} {tuple(want)} on {k.device} "
                                  f"(got {t.dtype} {tuple(t.shape)} on {t.device})")
         object.__setattr__(self, "_c", _KvCache(
             k.data_ptr(), v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(), table.data_ptr(),
@@ -322,7 +323,7 @@ def _list(device: torch.device, name: str, t: torch.Tensor | None, n: int | None
     """Address of a list of n int32 on the cache's device."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.dim() != 1 or t.device != device or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.get_device() != device.index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous 1-D int32 tensor on {device}")
     if n is not None and t.shape[0] != n:
         raise ValueError(f"{name} has {t.shape[0]} entries, expected {n}")
@@ -372,7 +373,7 @@ def cache_write(cache: PagedCache, seqs: torch.Tensor, starts: torch.Tensor, k: 
     n = seqs.numel()
     _, _, heads, _, dim = cache.k.shape
     for name, t in (("k", k), ("v", v)):
-        if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1:] != (heads, dim) or t.device != dev:
+        if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape[1:] != (heads, dim) or t.get_device() != dev.index:
             raise ValueError(f"{name} must be bfloat16 [tokens, {heads}, {dim}] on {dev}")
         if t.stride(2) != 1 and t.numel() > 0:
             raise ValueError(f"{name}'s innermost dimension must be contiguous")
@@ -399,7 +400,7 @@ def cache_gather(cache: PagedCache, seqs: torch.Tensor, starts: torch.Tensor | N
     if v is None:
         v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     for name, t in (("k", k), ("v", v)):
-        if t.shape != shape or t.dtype != torch.bfloat16 or t.device != dev or not t.is_contiguous():
+        if t.shape != shape or t.dtype is not torch.bfloat16 or t.get_device() != dev.index or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous bf16 tensor {shape} on {dev}")
     _call(dev, _lib.bsmt_cache_gather, c, int(layer), _list(dev, "seqs", seqs), _list(dev, "starts", starts, n), n,
           _list(dev, "cu_seqlens", cu_seqlens, n + 1), shape[0], k.data_ptr(), v.data_ptr())
@@ -455,7 +456,7 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, seqs: torch.Tensor, cu_s
     Returns (out bf16 [T, Hq, D], lse fp32 [Hq, T]); rows that see nothing get 0
     and -inf. No gradient flows to the cache."""
     c, device = _on_gpu(cache)
-    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.device != device or not q.is_contiguous():
+    if q.dtype is not torch.bfloat16 or q.dim() != 3 or q.get_device() != device.index or not q.is_contiguous():
         raise ValueError(f"q must be a contiguous bf16 tensor [tokens, Hq, D] on {device}")
     T, Hq, D = q.shape
     if D != cache.k.shape[4]:
