@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
     const KvCache& c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
-    asm volatile("griddepcontrol.launch_dependents;");  // the combining kernel may take its place, and waits for this one's end
+    asm volatile("griddepcontrol.launch_dependents;");  // the combining kernel may take its place and wait for this one's end
     uint8_t* const smem = smem_raw + (1024u - (shared_addr(smem_raw) & 1023u)) % 1024u;  // (the swizzle's period)
     const uint32_t bars = shared_addr(s_bars) + warp * 2 * Shape::kDeep * 8;
     if (lane < 2 * Shape::kDeep) bar_init(bars + lane * 8);
@@ -287,6 +287,8 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&k_map)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&v_map)) : "memory");
     }
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // what the stream's earlier kernels wrote is there
 
     // ---- this block's share of all tiles
     const int per_thread = (p.n + kBlockThreads - 1) / kBlockThreads;
@@ -973,6 +975,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(const
     constexpr int kPer = D / 32;  // columns of one lane
     constexpr int kFew = 16;
     __shared__ float s_o[kCombineWarps][D];
+    asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4* hd = reinterpret_cast<const int4*>(p.heads_of_parts + blockIdx.x * 8);
     const int4 h0 = hd[0];

@@ -207,7 +207,9 @@ extern "C" bsmt_status bsmt_rotary(const bsmt_rotary_spec* spec, int32_t dtype, 
         if (B * T > 0 && x.heads > 0 && (!x.in || !x.out)) return fail(BSMT_ERR_INVALID_ARGUMENT, "rotary: tensor %d is NULL", i);
         if (!aligned(x.in, size) || !aligned(x.out, size)) return fail(BSMT_ERR_INVALID_ARGUMENT, "rotary: tensor %d is misaligned", i);
         wide = wide && aligned(x.in, 16) && aligned(x.out, 16);
-        for (int j = 0; j < 3; ++j) wide = wide && x.in_strides[j] * size % 16 == 0 && x.out_strides[j] * size % 16 == 0;
+        const int64_t extents[3] = {B, x.heads, T};
+        for (int j = 0; j < 3; ++j)
+            wide = wide && (extents[j] <= 1 || (x.in_strides[j] * size % 16 == 0 && x.out_strides[j] * size % 16 == 0));
         p.x[i] = {x.in, x.out, x.in_strides[0], x.in_strides[1], x.in_strides[2], x.out_strides[0], x.out_strides[1], x.out_strides[2], x.heads};
         heads += x.heads;
     }
@@ -275,8 +277,8 @@ extern "C" bsmt_status bsmt_cache_write(const bsmt_kv_cache* cache, int32_t laye
     TRY(check_list("cu_seqlens", cu_seqlens, 1, true));
     if (n == 0 || T == 0) return ok();
     if (!k || !v || !k_strides || !v_strides) return fail(BSMT_ERR_INVALID_ARGUMENT, "k, v and their strides must be non-NULL");
-    for (int i = 0; i < 2; ++i)
-        if (k_strides[i] % 8 != 0 || v_strides[i] % 8 != 0 || k_strides[i] < 0 || v_strides[i] < 0)
+    for (int i = 0; i < 2; ++i)  // (the stride of one token or head is not used)
+        if ((i == 0 ? T : p.c.heads) > 1 && (k_strides[i] % 8 != 0 || v_strides[i] % 8 != 0 || k_strides[i] < 0 || v_strides[i] < 0))
             return fail(BSMT_ERR_INVALID_ARGUMENT, "k and v strides must be multiples of 8 elements");
     if (!aligned(k, 16) || !aligned(v, 16)) return fail(BSMT_ERR_INVALID_ARGUMENT, "k and v must be 16-byte aligned");
     int dev = 0, nsm = 0;
@@ -493,19 +495,24 @@ bsmt_status launch_paged(int dev, int nsm, bsmt::PagedParams p, const bsmt::Mask
     CUtensorMap k_map, v_map;
     TRY(encode_rows(&k_map, p.c.k, rows, D, std::min(p.c.page, bsmt::kTileTokens)));
     TRY(encode_rows(&v_map, p.c.v, rows, D, std::min(p.c.page, bsmt::kTileTokens)));
-    kern<<<blocks, 32 * bsmt::PagedShape<D, NT>::kWarps, smem, s>>>(p, dnf, k_map, v_map);
-    TRY(launched("paged_attention"));
-    // The combining kernel is set up while the first one runs, and waits for its end on the device.
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks, 2 * NT);
-    cfg.blockDim = dim3(32 * bsmt::kCombineWarps);
-    cfg.stream = s;
+    // Each kernel is set up while the one before it in the stream runs, and waits for that one's end on the device
+    // before it reads anything.
     cudaLaunchAttribute early;
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(32 * bsmt::PagedShape<D, NT>::kWarps);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, bsmt::paged_combine_kernel<D, 8 * NT>, p);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, dnf, k_map, v_map);
+    if (e != cudaSuccess) return fail(BSMT_ERR_CUDA, "paged_attention launch: %s", cudaGetErrorString(e));
+    cfg.gridDim = dim3(blocks, 2 * NT);
+    cfg.blockDim = dim3(32 * bsmt::kCombineWarps);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, bsmt::paged_combine_kernel<D, 8 * NT>, p);
     if (e != cudaSuccess) return fail(BSMT_ERR_CUDA, "paged_attention combine launch: %s", cudaGetErrorString(e));
     TRY(launched("paged_attention combine"));
     return BSMT_OK;

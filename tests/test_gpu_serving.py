@@ -118,3 +118,46 @@ def test_training_step_through_rotary_and_attention():
         # the library's backward tolerance: 2e-2 of the tensor's largest gradient
         err, top = (a.grad.cpu().double() - w.grad).abs().max().item(), max(1.0, w.grad.abs().max().item())
         assert err <= 2e-2 * top, (name, err)
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+def test_captured_decode_step(code):
+    # extend, rotary, write and attention of a padded batch in one CUDA graph, replayed as the sequences grow
+    gen = torch.Generator().manual_seed(3)
+    spec = bsmt.rotary_spec(D, [16, 16])
+    b = Both(60, HKV, D, 6, 12, 16, 1, code)
+    b.add([0, 1, 2, 3], [15, 1, 40, 100])
+    n = 5
+    seqs = ints([2, 0, -1, 3, 1])
+    fused = torch.empty((n, HQ + 2 * HKV, D), dtype=torch.bfloat16, device="cuda")
+    source = torch.empty_like(fused)
+    pos = torch.zeros((2, n), dtype=torch.int32, device="cuda")
+    starts = torch.empty(n, dtype=torch.int32, device="cuda")
+    mask = bsmt.and_masks(bsmt.causal(), bsmt.or_masks(bsmt.sink(3), bsmt.sliding_window(50)))
+
+    def step():
+        fused.copy_(source)
+        bsmt.cache_extend(b.dev, seqs, None, starts)
+        q, k = bsmt.rotary(fused[:, :HQ], fused[:, HQ:HQ + HKV], pos, spec)
+        bsmt.cache_write(b.dev, seqs, starts, k, fused[:, HQ + HKV:])
+        return k, q, bsmt.paged_attention(q, b.dev, seqs, mask_mod=mask, enable_gqa=True)
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        k, q, (out, lse) = step()
+    for i in range(12):
+        if i == 6:
+            seqs.copy_(ints([3, -1, 1, 4, 0]))
+        now = seqs.tolist()
+        x = torch.randn((n, HQ + 2 * HKV, D), generator=gen).bfloat16()
+        source.copy_(x)
+        at = torch.tensor([max(0, int(b.ref.seq_lens[s])) if s >= 0 else 0 for s in now], dtype=torch.int32)
+        pos.copy_(torch.stack([at, at // 3]))
+        g.replay()
+        want = b.ref.extend(now, [1] * n)
+        assert starts.tolist() == want
+        b.ref.write(0, now, want, k.double().cpu().numpy(), x[:, HQ + HKV:].double().numpy(), range(n + 1))
+        b.equal()
+        tree = ("and", ("causal",), ("or", ("sink", 3), ("window", 50)))
+        o, ls = osv.paged_attention(q.double().cpu().numpy(), b.ref, now, range(n + 1), tree, ())
+        b.close(out, lse, o, ls, q.cpu())

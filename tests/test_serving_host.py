@@ -69,8 +69,9 @@ def test_null_cache_and_lists():
     for args in ((None, FAKE, 1, None, FAKE, FAKE, 1, st, st), (FAKE, None, 1, None, FAKE, FAKE, 1, st, st),
                  (FAKE + 2, FAKE, 1, None, FAKE, FAKE, 1, st, st), (FAKE, FAKE, -1, None, FAKE, FAKE, -1, st, st),
                  (FAKE, FAKE, 1, None, None, FAKE, 1, st, st), (FAKE, FAKE, 1, None, FAKE, FAKE + 8, 1, st, st),
-                 (FAKE, FAKE, 1, None, FAKE, FAKE, 1, strides(516, 128), st),
-                 (FAKE, FAKE, 1, None, FAKE, FAKE, 1, st, strides(-512, 128)), (FAKE, FAKE, 1, FAKE + 1, FAKE, FAKE, 9, st, st)):
+                 (FAKE, FAKE, 2, None, FAKE, FAKE, 2, strides(516, 128), st),
+                 (FAKE, FAKE, 2, None, FAKE, FAKE, 2, st, strides(-512, 128)),
+                 (FAKE, FAKE, 1, None, FAKE, FAKE, 1, strides(512, 100), st), (FAKE, FAKE, 1, FAKE + 1, FAKE, FAKE, 9, st, st)):
         assert _lib.bsmt_cache_write(c, 0, *args, None) == INVALID, args
     # without offsets there is one token for each sequence
     assert _lib.bsmt_cache_write(c, 0, FAKE, FAKE, 2, None, FAKE, FAKE, 3, st, st, None) == SHAPE
