@@ -286,32 +286,37 @@ __global__ void __launch_bounds__(256) cache_write_rows_kernel(const __grid_cons
 // heads of 128 in 64 us (4.5 TB/s; 69 us with the three blocks an SM that 80 registers leave).
 template <int NV, bool INT8>
 __global__ void __launch_bounds__(256, NV <= 4 ? 4 : 2) cache_write_pages_kernel(const __grid_constant__ CacheWriteParams p) {
-    __shared__ uint32_t s_most[2][8];
+    __shared__ __align__(16) uint32_t s_most[2][8];
     const KvCache& c = p.c;
     const int groups = (2 * c.heads + p.share - 1) / p.share;
     const int64_t item = blockIdx.x / groups;
     CacheItem it;
     if (!cache_item(p, item, threadIdx.x == 0, it)) return;
     const int u0 = static_cast<int>(blockIdx.x - item * groups) * p.share, u1 = min(2 * c.heads, u0 + p.share);
-    const int vecs = c.dim / 8, shift = c.dim == 128 ? 4 : 3;
-    const int all = it.rows * vecs;
+    // the thread's vectors: one column of 8 values, every `step`th row
+    const int shift = c.dim == 128 ? 4 : 3, row = threadIdx.x >> shift, step = 256 >> shift;
+    const int col = (threadIdx.x & ((1 << shift) - 1)) * 8;
+    const __nv_bfloat16* const k0 = p.k + (it.token + row) * p.kt + col;
+    const __nv_bfloat16* const v0 = p.v + (it.token + row) * p.vt + col - static_cast<int64_t>(c.heads) * p.vh;
+    const int64_t k_step = step * p.kt, v_step = step * p.vt;
+    const int64_t head_bytes = static_cast<int64_t>(c.page) * c.dim, at = it.place * c.heads;  // of the page's first head
     auto load = [&](int u, uint4 w[NV]) {
         const bool is_v = u >= c.heads;
-        const int64_t src_row = is_v ? p.vt : p.kt;
-        const __nv_bfloat16* src = (is_v ? p.v + (u - c.heads) * p.vh : p.k + u * p.kh) + it.token * src_row;
+        const __nv_bfloat16* src = is_v ? v0 + u * p.vh : k0 + u * p.kh;
+        const int64_t next_row = is_v ? v_step : k_step;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int x = threadIdx.x + 256 * j;
-            w[j] = x < all ? *reinterpret_cast<const uint4*>(src + (x >> shift) * src_row + (x & (vecs - 1)) * 8) : make_uint4(0, 0, 0, 0);
+            w[j] = row + j * step < it.rows ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
+            src += next_row;
         }
     };
     uint4 now[NV], next[NV];
     load(u0, now);
     for (int u = u0; u < u1; ++u) {
         const bool is_v = u >= c.heads;
-        const int head = is_v ? u - c.heads : u;
-        uint8_t* dst = (is_v ? c.v : c.k) + it.place * page_elems(c) + static_cast<int64_t>(head) * c.page * c.dim;
-        float* scale = (is_v ? c.v_scale : c.k_scale) + it.place * c.heads + head;
+        const int64_t place = at + (is_v ? u - c.heads : u);
+        float* scale = (is_v ? c.v_scale : c.k_scale) + place;
+        uint8_t* codes = (is_v ? c.v : c.k) + place * head_bytes;
         const float held = it.row0 > 0 ? *scale : 0.f;
         if (u + 1 < u1) load(u + 1, next);
         uint32_t both = 0;
@@ -328,16 +333,14 @@ __global__ void __launch_bounds__(256, NV <= 4 ? 4 : 2) cache_write_pages_kernel
         uint32_t most = __reduce_max_sync(0xFFFFFFFFu, max(both & 0xFFFFu, both >> 16));
         if ((threadIdx.x & 31) == 0) s_most[u & 1][threadIdx.x >> 5] = most;
         __syncthreads();
-#pragma unroll
-        for (int w = 0; w < 8; ++w) most = max(most, s_most[u & 1][w]);
+        const uint4 m0 = *reinterpret_cast<const uint4*>(s_most[u & 1]), m1 = *reinterpret_cast<const uint4*>(s_most[u & 1] + 4);
+        most = max(max(max(m0.x, m0.y), max(m0.z, m0.w)), max(max(m1.x, m1.y), max(m1.z, m1.w)));
         float inv;
-        const float used = page_scale<INT8>(most, held, it.row0, dst, c.dim, threadIdx.x, 256, &inv);
-        dst += static_cast<int64_t>(it.row0) * c.dim;
+        const float used = page_scale<INT8>(most, held, it.row0, codes, c.dim, threadIdx.x, 256, &inv);
+        uint8_t* dst = codes + it.row0 * c.dim + threadIdx.x * 8;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int x = threadIdx.x + 256 * j;
-            if (x < all) *reinterpret_cast<uint2*>(dst + x * 8) = encode8<INT8>(now[j], inv, plain);
-        }
+        for (int j = 0; j < NV; ++j)
+            if (row + j * step < it.rows) *reinterpret_cast<uint2*>(dst + j * 2048) = encode8<INT8>(now[j], inv, plain);
         if (threadIdx.x == 0) *scale = used;
 #pragma unroll
         for (int j = 0; j < NV; ++j) now[j] = next[j];
