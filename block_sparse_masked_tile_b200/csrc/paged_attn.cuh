@@ -22,9 +22,9 @@
 // the 16 rows of mma.sync m16n8k16, the query rows its 8 columns. A decoded token
 // has few rows, so this wastes less of the unit, and half the registers, of the
 // other order. P^T goes from the first product's result to the second's operand
-// by movmatrix. Codes become halves exactly (e4m3 by cvt, int8 by byte permutes); q, scaled by
-// a power of two for each row, becomes halves exactly down to 2^-28 of the row's
-// largest value. tcgen05 takes 8-bit operands only in pairs, which would round q
+// by movmatrix. Codes become halves exactly (e4m3 by cvt, int8 by byte permutes);
+// q, scaled by a power of two for each row, becomes halves exactly down to 2^-28
+// of the row's largest value. tcgen05 takes 8-bit operands only in pairs, which would round q
 // and P to 8 bits, and 16-bit ones from shared or tensor memory, which would cost
 // a write of every converted tile; eight rows need no such rate.
 //
@@ -67,10 +67,8 @@ struct PagedParams {
 };
 
 // Three blocks an SM with 16 KB of slots a warp; with NT = 4 (D = 64 alone) two with
-// 24 KB. (NT = 2 at D = 128 has 168 registers and
-// some spills in three blocks, none in two: 338 and 378 us for 24 sequences up to
-// 64k with 16 rows each; five warps in two blocks 401 us.) A slot holds the K or the V
-// codes of a tile.
+// 24 KB. (NT = 2 at D = 128, 24 sequences up to 64k with 16 rows each: 326 us in three
+// blocks of 168 registers, 363 in two of 255.) A slot holds the K or the V codes of a tile.
 template <int D, int NT>
 struct PagedShape {
     static constexpr int kBlocks = NT > 2 ? 2 : 3;  // of an SM

@@ -599,8 +599,8 @@ extern "C" bsmt_status bsmt_paged_attention(const void* q, int64_t T, int64_t Hq
     p.alibi_h0 = sa.alibi_h0;
     p.alibi_heads = sa.alibi_heads;
     // Row tiles of 8 or 16, or, at D = 64, 32: the smallest that holds an average sequence's rows, so that its keys are
-    // read once. (32 rows of 24 sequences up to 64k: 16 a tile 433 us at D = 64, 588 at D = 128, where O spills with 32;
-    // 32 a tile 392 and 668.)
+    // read once. (32 rows of 24 sequences up to 64k: 32 a tile 377 us and 16 a tile 438 us at D = 64; at D = 128 O spills
+    // with 32, which took 1.14 times as long as two tiles of 16.)
     const int64_t rows = (T * p.group + std::max<int64_t>(n, 1) - 1) / std::max<int64_t>(n, 1);
     const int nt = rows <= 8 ? 1 : rows <= 16 || p.c.dim == 128 ? 2 : 4;
     const int mods = sa.mode <= 1 ? sa.mode : 2;
