@@ -245,7 +245,7 @@ struct PagedSeqShared {
 
 // A unit weighs its tiles and what it costs to begin and end one, in tiles. A
 // sequence without a key still has one (empty) tile, which writes its rows.
-constexpr int kUnitCost = 10;  // (0, 6, 12: ragged batch of 64 sequences up to 16k 215, 201, 200 us)
+constexpr int kUnitCost = 10;  // (6, 10, 16: ragged batch of 64 up to 16k 195, 194, 197 us; 4 + 1024 visible of 64 up to 32k 46.7, 46.0, 46.8)
 template <int ROWS>
 __device__ __forceinline__ int64_t paged_weight(const PagedParams& p, const PagedSeq& s, int tiles) {
     if (s.count == 0) return 0;
