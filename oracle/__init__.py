@@ -31,6 +31,9 @@ What it computes is the plain definition of each operation:
   tensorplay.nn.attention page, BlockMask "Details" items 3-4: dK and dV walk
   the mask along the query dimension).
 
+* ``serving`` has rotary positions, a model of the 8-bit paged cache and
+  attention over it, each as the loop that its definition says.
+
 Parity: every function here is pinned by tests in ``tests/test_oracle_*.py``
 against closed forms, library routines on special cases and invariants. The
 score_mod values are pinned only by closed-form cases (ALiBi on a constant

@@ -163,10 +163,11 @@ def test_large_small_and_non_finite_queries():
     assert torch.isfinite(out[2, 1]).all() and torch.isfinite(out[3, 0]).all()
 
 
-@pytest.mark.parametrize("count, group", [(6, 4), (1, 4)])
-def test_masked_nan_does_not_reach_the_result(count, group):
-    b = filled([90], 2, 128, 32, "e4m3")
-    q = queries(count, 2 * group, 128)
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("count, group", [(6, 4), (3, 4), (1, 4)])  # row tiles of 16 or 32, 16, 8
+def test_masked_nan_does_not_reach_the_result(count, group, dim):
+    b = filled([90], 2, dim, 32, "e4m3")
+    q = queries(count, 2 * group, dim)
     clean, _ = b.attend(q, [0], [count], STREAM)
     # NaN where no query looks: behind the end, between the sinks and the window
     d = b.dev
