@@ -950,7 +950,7 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
         // ---- the next sequence that has queries
         off = 0;
         if (left <= 0) break;
-        do {
+        while (true) {
             if (++i >= p.n) return;
             if (per_thread == 1) {
                 if (tid == i) describe(own);
@@ -959,7 +959,9 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
                 describe(own);
             }
             __syncthreads();
-        } while (s_seq.weight == 0);
+            if (s_seq.weight != 0) break;
+            __syncthreads();  // every thread has read it before the next description is written over it
+        }
     }
 }
 
