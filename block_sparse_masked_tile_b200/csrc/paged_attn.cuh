@@ -32,6 +32,7 @@
 // sum l, and mo of score + log2(v_scale), for O, so that P * v_scale, a half, stays
 // in range whatever the pages' scales are. They follow the running maxima lazily.
 #pragma once
+#include <cfloat>
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -654,21 +655,25 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
                     }
                     if (MODS == 1) {
                         // cap * tanh(z / cap), in units of log2. Up to a cap of 64 the exponential's form alone: its error
-                        // is cap * 2^-23, below a score's own. Beyond, a score may be small beside the cap.
-                        const float cap2 = p.cap * kLog2e, inv = 1.f / p.cap;
+                        // is cap * 2^-23, below a score's own, and all factors go into one (at most the largest float, so
+                        // that a product q . k of 0 stays 0). Beyond, a score may be small beside the cap, and 1 / cap
+                        // times the row's and the page's scales too small for a float: z comes first.
+                        const float inv = fminf(1.f / p.cap, FLT_MAX);
 #pragma unroll
                         for (int r = 0; r < NT; ++r)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                const float u[2] = {qs[r][0] * ks[h] * inv, qs[r][1] * ks[h] * inv};
+                                const float u[2] = {qs[r][0] * ks[h], qs[r][1] * ks[h]};
                                 if (p.cap <= 64.f) {
-                                    const float w[2] = {u[0] * (2.f * kLog2e), u[1] * (2.f * kLog2e)};
+                                    const float cap2 = p.cap * kLog2e;
+                                    const float w[2] = {fminf(u[0] * inv * (2.f * kLog2e), FLT_MAX), fminf(u[1] * inv * (2.f * kLog2e), FLT_MAX)};
 #pragma unroll
                                     for (int e = 0; e < 4; ++e)
                                         s[r][h][e] = fmaf(-2.f * cap2, rcp_fast(exp2_fast(s[r][h][e] * w[e & 1]) + 1.f), cap2);
                                 } else {
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e) s[r][h][e] = cap2 * tanh_fast(s[r][h][e] * u[e & 1]);
+                                    for (int e = 0; e < 4; ++e)
+                                        s[r][h][e] = p.cap * tanh_fast(s[r][h][e] * u[e & 1] * inv) * kLog2e;
                                 }
                             }
                     } else if (MODS == 2) {

@@ -39,3 +39,38 @@ def test_runs_of_sequences_without_queries(dim, group, n, first):
         again = bsmt.paged_attention(qd, b.dev, seqs, cu, bsmt.causal(), enable_gqa=True)
         assert torch.equal(again[0], out) and torch.equal(again[1], lse)
     bsmt.check_device_status()
+
+
+@pytest.mark.parametrize("also", [(), (("alibi", None),)])
+@pytest.mark.parametrize("cap", [1e-44, 1e-39, 1e-30, 1e36, 1e38, 2.4e38, 3.4e38])
+def test_soft_caps_at_the_ends_of_fp32(cap, also):
+    lens = [150, 33]
+    b = filled(lens, 2, 64, 32, "e4m3")
+    q = queries(4, 4, 64)
+    out, lse = b.attend(q, [0, 1], [2, 2], ("causal",), (("softcap", cap),) + also)
+    if cap < 1 and not also:  # every score is (nearly) 0
+        want = torch.tensor([float(n - 1 + i) for n in lens for i in range(2)]).log()
+        assert ((lse.cpu() - want).abs() <= 2e-6 * want).all()
+
+
+def test_soft_cap_far_below_large_scores():
+    # scores beyond any float over the cap, and products q . k of 0 among them (a token of zeros in the query's elements)
+    b = filled([60], 1, 64, 32, "int8")
+    k = b.values(3)
+    k[1, :, 32:] = 0
+    starts = b.extend([0], [3])
+    b.write(0, [0], starts, k, b.values(3), [3])
+    q = queries(2, 4, 64)
+    q[:, :, :32] = 0
+    q[0] *= 2.0 ** 110
+    cap = 2.0 ** -100
+    out, lse = bsmt.paged_attention(q.cuda(), b.dev, ints([0]), ints([0, 2]), bsmt.causal(), bsmt.softcap(cap), enable_gqa=True)
+    bsmt.check_device_status()
+    # scores of magnitude 2^-100: the mean of the values, to P's 11 bits and bf16's half step
+    n = torch.tensor([62.0, 63.0])
+    assert ((lse.cpu() - n.log()).abs() <= 2e-6 * n.log()).all()
+    v = b.ref.tokens(0, 0, 0, 63)[1][:, 0]
+    for t in range(2):
+        want = v[:62 + t].mean(0)
+        top = np.abs(v).max()
+        assert (np.abs(out[t].double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -14) * top).all()
