@@ -202,11 +202,11 @@ struct PagedSeq {
 
 __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int i) {
     PagedSeq s;
-    s.slot = __ldg(p.seqs + i);
+    s.slot = p.seqs[i];
     int64_t q0 = i, q1 = i + 1;
     if (p.cu != nullptr) {
-        q0 = __ldg(p.cu + i);
-        q1 = __ldg(p.cu + i + 1);
+        q0 = p.cu[i];
+        q1 = p.cu[i + 1];
         if (q0 < 0 || q1 < q0 || q1 > p.T) {
             set_status(p.status, BSMT_ERR_DEVICE_PRECONDITION);
             q1 = q0;
@@ -219,7 +219,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedParams& p, int i) {
         if (s.slot != -1) set_status(p.status, BSMT_ERR_DEVICE_BOUNDS);
         s.slot = -1;
     } else {
-        const int64_t len = __ldg(p.c.seq_lens + s.slot);
+        const int64_t len = p.c.seq_lens[s.slot];
         if (len < 0 || len > seq_capacity(p.c))
             set_status(p.status, BSMT_ERR_DEVICE_BOUNDS);
         else
@@ -287,7 +287,9 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&v_map)) : "memory");
     }
 
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // what the stream's earlier kernels wrote is there
+    // What the stream's earlier kernels wrote is there. (Plain loads below, no __ldg: these data may be written while this
+    // kernel waits here, and only loads that are not taken for constant stay behind the wait.)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // ---- this block's share of all tiles
     const int per_thread = (p.n + kBlockThreads - 1) / kBlockThreads;
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
     if (tid == 0) p.heads_of_parts[blockIdx.x * 8] = 0;
     // rows behind the last sequence belong to none: they see nothing
     if (p.cu != nullptr) {
-        const int64_t used = max(0, min(__ldg(p.cu + p.n), static_cast<int>(p.T)));
+        const int64_t used = max(0, min(p.cu[p.n], static_cast<int>(p.T)));
         if (used < p.T) {
             const int64_t stride = static_cast<int64_t>(gridDim.x) * kBlockThreads;
             const int64_t rest = (p.T - used) * p.Hq;
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
             };
             auto page_at = [&](int tok) -> int {  // page of a token; -1: behind the sequence
                 if (tok < 0 || tok >= len) return -1;
-                return __ldg(table + (tok >> c.page_shift));
+                return table[tok >> c.page_shift];
             };
             // the page of the tile's second half: another one with pages of 16
             auto second_page = [&](int tok, int first) -> int { return c.page == 16 ? page_at(tok < 0 ? -1 : tok + 16) : first; };
@@ -460,7 +462,7 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
                     if ((!ok_a || (!ok_b && next_tok + 16 < len)) && lane == 0) set_status(p.status, BSMT_ERR_DEVICE_BOUNDS);
                     row_a[x] = ok_a ? ((p.layer * c.pages + next_a) * c.heads + head) * c.page + (next_tok & (c.page - 1)) : no_row;
                     row_b[x] = ok_b ? ((p.layer * c.pages + next_b) * c.heads + head) * c.page + ((next_tok + 16) & (c.page - 1)) : no_row;
-                    scale_q[x] = ((lane & 1) ? ok_b : ok_a) ? __ldg(lane_scales + static_cast<int64_t>((lane & 1) ? next_b : next_a) * c.heads + head) : 0.f;
+                    scale_q[x] = ((lane & 1) ? ok_b : ok_a) ? lane_scales[static_cast<int64_t>((lane & 1) ? next_b : next_a) * c.heads + head] : 0.f;
                     load(&k_map, slot, bar, row_a[x], row_b[x]);
                 }
             };
@@ -489,8 +491,8 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
                     const uint4* src = reinterpret_cast<const uint4*>(p.q + ((s_seq.s.q0 + qi) * p.Hq + hq) * D + 16 * t);
 #pragma unroll
                     for (int x = 0; x < kChunks; ++x) {
-                        q_raw[r][x][0] = valid ? __ldg(src + 8 * x) : make_uint4(0, 0, 0, 0);
-                        q_raw[r][x][1] = valid ? __ldg(src + 8 * x + 1) : make_uint4(0, 0, 0, 0);
+                        q_raw[r][x][0] = valid ? src[8 * x] : make_uint4(0, 0, 0, 0);
+                        q_raw[r][x][1] = valid ? src[8 * x + 1] : make_uint4(0, 0, 0, 0);
                     }
                 }
                 uint32_t slot = slot_k, bar = bar_k;
@@ -567,7 +569,7 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
                         if (row0 + col < rows_all) {
                             const int h = head * p.group + in_group + col - (pos[r][y] - (len - count) - static_cast<int>(qi0)) * p.group;
                             slope[r][y] = p.slopes != nullptr
-                                              ? __ldg(p.slopes + h)
+                                              ? p.slopes[h]
                                               : exp2f(-8.f * static_cast<float>(p.alibi_h0 + h + 1) / static_cast<float>(p.alibi_heads));
                         }
                     }

@@ -74,3 +74,33 @@ def test_soft_cap_far_below_large_scores():
         want = v[:62 + t].mean(0)
         top = np.abs(v).max()
         assert (np.abs(out[t].double().cpu().numpy() - want) <= 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -14) * top).all()
+
+
+@pytest.mark.parametrize("dim, group, count", [(128, 4, 1), (64, 4, 6), (128, 4, 6)])
+def test_outputs_as_the_next_calls_queries(dim, group, count):
+    # Each call may be set up while the one before it runs, and reads what that one's last kernel writes: the outputs of
+    # units that blocks share, in two buffers in turn.
+    lens = [9000, 700, 20000, 31]
+    b = filled(lens, 2, dim, 64, "e4m3")
+    seqs, cu = ints([2, 0, 3, 1]), ints(running([count] * 4))
+    start = queries(4 * count, 2 * group, dim).cuda()
+    lse = torch.empty((2 * group, 4 * count), device="cuda")
+    ws = torch.empty(bsmt.paged_attention_workspace_bytes(dim), dtype=torch.uint8, device="cuda")
+
+    def chain(wait):
+        a, c = start.clone(), torch.empty_like(start)
+        got = []
+        for _ in range(12):
+            bsmt.paged_attention(a, b.dev, seqs, cu, bsmt.causal(), None, 4.0, True, out=c, lse=lse, workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+                got.append(c.clone())
+                torch.cuda.synchronize()
+            a, c = c, a
+        return a, got
+
+    want, steps = chain(True)
+    assert all(not torch.equal(x, y) for x, y in zip(steps, steps[1:]))
+    for _ in range(20):
+        assert torch.equal(chain(False)[0], want)
+    bsmt.check_device_status()
