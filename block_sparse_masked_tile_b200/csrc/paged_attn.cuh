@@ -47,7 +47,11 @@ namespace bsmt {
 
 constexpr int kCombineWarps = 4;
 constexpr int kTileTokens = 32;
-constexpr float kLazy = 8.f;  // log2 by which a score may pass its reference: P stays below 2^8, far inside a half
+constexpr float kLazy = 8.f;  // log2 by which a score may pass its reference
+// log2 by which O's reference stays below the largest score + log2(v_scale): P * v_scale then lies below 2^(8 + 7), inside
+// a half, and a half's smallest step, 2^-24, is 2^-31 of the largest term: many small terms beside one large one count.
+constexpr float kRoom = 7.f;
+constexpr float kRoomInv = 0x1p-7f;
 
 struct PagedParams {
     KvCache c;
@@ -634,7 +638,7 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
                     }
                     const float ks[2] = {__shfl_sync(0xFFFFFFFFu, scale_q[0], 0), __shfl_sync(0xFFFFFFFFu, scale_q[0], 1)};
                     const float vs[2] = {__shfl_sync(0xFFFFFFFFu, scale_q[0], 2), __shfl_sync(0xFFFFFFFFu, scale_q[0], 3)};
-                    const float ev[2] = {__log2f(fmaxf(vs[0], 0x1p-126f)), __log2f(fmaxf(vs[1], 0x1p-126f))};
+                    const float ev[2] = {__log2f(fmaxf(vs[0], 0x1p-120f)), __log2f(fmaxf(vs[1], 0x1p-120f))};  // (so that m - mo is at most 127)
 
                     // which keys the rows see
                     bool clean = clean_lo <= tok && tok + kTileTokens - 1 <= clean_hi;
@@ -717,7 +721,7 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
                             for (int h = 0; h < 2; ++h) {
                                 f[r][y][h] = MODS != 0 ? 1.f : fmaxf(qs[r][y] * ks[h], 1e-37f);
                                 const float top = fmaxf(s[r][h][y], s[r][h][2 + y]) * f[r][y][h];
-                                grows = grows || top > m[r][y] + kLazy || top + ev[h] > mo[r][y] + kLazy;
+                                grows = grows || top > m[r][y] + kLazy || top + ev[h] > mo[r][y] + (kLazy + kRoom);
                             }
                     if (__any_sync(0xFFFFFFFFu, grows)) {
 #pragma unroll
@@ -734,7 +738,7 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
                                     top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], 16));
                                 }
                                 const float mn = fmaxf(m[r][y], fmaxf(top[0], top[1]));
-                                const float mon = fmaxf(mo[r][y], fmaxf(top[0] + ev[0], top[1] + ev[1]));
+                                const float mon = fmaxf(mo[r][y], fmaxf(top[0] + ev[0], top[1] + ev[1]) - kRoom);
                                 const float ref = mn == -INFINITY ? 0.f : mn, refo = mon == -INFINITY ? 0.f : mon;
                                 l[r][y] *= exp2_fast(m[r][y] - ref);
                                 ao[y] = exp2_fast(mo[r][y] - refo);
@@ -777,7 +781,8 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
                                     e[y] = exp2_fast(MODS != 0 ? s[r][h][2 * z + y] - ref[y] : fmaf(s[r][h][2 * z + y], f[r][y][h], -ref[y]));
                                     l[r][y] += e[y];
                                 }
-                                // P to 11 bits: an error of 2^-12 of each term, below the output's bf16 rounding
+                                // P to a half: an error of 2^-12 of each term down to 2^-21 of the largest, of 2^-32 of the
+                                // largest for smaller ones, below the output's bf16 rounding for up to 2^22 keys
                                 pb[r][h][z] = transpose8x8(pack_half2(e[0] * (vs[h] * shift[0]), e[1] * (vs[h] * shift[1])));
                             }
                     }
@@ -936,8 +941,9 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
                     const int64_t token = s_seq.s.q0 + qi0 + up_q;
                     const int hq = head * p.group + in_group + row - up_q * p.group;
                     // (a NaN sum is a row whose scores are NaN)
-                    const float f = sum == 0.f ? 0.f : exp2_fast(refo - ref) / sum;
-                    const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * f, acc.y * f), b = __floats2bfloat162_rn(acc.z * f, acc.w * f);
+                    const float f = sum == 0.f ? 0.f : exp2_fast(refo + kRoom - ref) / sum;
+                    const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * kRoomInv * f, acc.y * kRoomInv * f),
+                                         b = __floats2bfloat162_rn(acc.z * kRoomInv * f, acc.w * kRoomInv * f);
                     *reinterpret_cast<uint2*>(p.out + (token * p.Hq + hq) * D + d) =
                         make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
                     if (d == 0) p.lse[static_cast<int64_t>(hq) * p.T + token] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
@@ -1045,10 +1051,10 @@ __global__ void __launch_bounds__(32 * kCombineWarps) paged_combine_kernel(const
             }
             if (warp != 0) continue;
         }
-        const float f = sum == 0.f ? 0.f : exp2_fast(refo - ref) / sum;
+        const float f = sum == 0.f ? 0.f : exp2_fast(refo + kRoom - ref) / sum;
         Pack<__nv_bfloat16, kPer> r;
 #pragma unroll
-        for (int y = 0; y < kPer; ++y) r.v[y] = __float2bfloat16_rn(acc[y] * f);
+        for (int y = 0; y < kPer; ++y) r.v[y] = __float2bfloat16_rn(acc[y] * kRoomInv * f);
         *reinterpret_cast<Pack<__nv_bfloat16, kPer>*>(p.out + (token * p.Hq + hq) * D + lane * kPer) = r;
         if (lane == 0) p.lse[static_cast<int64_t>(hq) * p.T + token] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
     }

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import block_sparse_masked_tile_b200 as bsmt
+from oracle import serving as osv
 from tests.serving_helpers import Both, ints, queries, running
 
 pytestmark = pytest.mark.gpu
@@ -104,3 +105,30 @@ def test_outputs_as_the_next_calls_queries(dim, group, count):
     for _ in range(20):
         assert torch.equal(chain(False)[0], want)
     bsmt.check_device_status()
+
+
+@pytest.mark.parametrize("dim, group", [(128, 1), (64, 12), (64, 30)])
+@pytest.mark.parametrize("far", [14.0, 20.0, 26.0])  # log2 by which the first token's weight is above each other's
+def test_many_small_weights_beside_a_large_one(dim, group, far):
+    # A first token that takes most of the weight and whose value is 0, as sinks do: the rest is the output. The sequence
+    # is listed so often that a block has all of its keys.
+    n, times = 16384, 500
+    b = Both(n // 128, 1, dim, 1, n // 128, 128, 1, "e4m3")
+    starts = b.extend([0], [n])
+    k, v = torch.zeros((n, 1, dim)), 0.75 + 0.5 * torch.rand((n, 1, dim), generator=b.gen)
+    k[0, 0, 0], v[0] = 4.0, 0.0
+    k[1:, 0, 1] = (torch.arange(1, n) % 4) * 0.25  # small differences among the others
+    b.write(0, [0], starts, k.bfloat16(), v.bfloat16(), [n])
+    q = torch.zeros((1, group, dim))
+    q[..., 0], q[..., 1] = far * float(np.log(2.0)) / 4.0, 0.5
+    q = q.bfloat16()
+    out, lse = bsmt.paged_attention(q.cuda().repeat(times, 1, 1), b.dev, ints([0] * times), None, None, None, 1.0, True)
+    bsmt.check_device_status()
+    want, want_lse = osv.paged_attention(q.double().numpy(), b.ref, [0], [0, 1], None, (), 1.0)
+    total = np.exp(want_lse[0, 0] - 4.0 * float(q[0, 0, 0]))  # of the weights, the first token's as 1
+    # bf16's half step (counted as 2^-8 of the output); P in halves: 2^-11 of each term, and for small ones half of the
+    # step 2^-24 where the largest term is 2^7 at least; 2^-14 for exp2, the scores' rounding and fp32 sums
+    top = float(np.abs(b.ref.tokens(0, 0, 0, n)[1]).max())
+    tol = (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -14) * np.abs(want) + n * 2.0 ** -32 * top / total
+    assert (np.abs(out.double().cpu().numpy() - want) <= tol).all(), (out[0, 0, :4], want[0, 0, :4])
+    assert (np.abs(lse.double().cpu().numpy() - want_lse) <= 1e-5 * np.abs(want_lse)).all()
