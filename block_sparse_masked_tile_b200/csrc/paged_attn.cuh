@@ -67,6 +67,7 @@ struct PagedParams {
     int64_t T;
     int32_t n, layer, Hq, group, min_share;
     float scale, cap;
+    float cap_inv;  // 2 log2(e) / cap up to a cap of 64, beyond 1 / cap; at most the largest float
     int32_t alibi_first, alibi_h0, alibi_heads, softcap;
     int* status;
 };
@@ -664,7 +665,6 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
                         // is cap * 2^-23, below a score's own, and all factors go into one (at most the largest float, so
                         // that a product q . k of 0 stays 0). Beyond, a score may be small beside the cap, and 1 / cap
                         // times the row's and the page's scales too small for a float: z comes first.
-                        const float inv = fminf(1.f / p.cap, FLT_MAX);
 #pragma unroll
                         for (int r = 0; r < NT; ++r)
 #pragma unroll
@@ -672,14 +672,14 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
                                 const float u[2] = {qs[r][0] * ks[h], qs[r][1] * ks[h]};
                                 if (p.cap <= 64.f) {
                                     const float cap2 = p.cap * kLog2e;
-                                    const float w[2] = {fminf(u[0] * inv * (2.f * kLog2e), FLT_MAX), fminf(u[1] * inv * (2.f * kLog2e), FLT_MAX)};
+                                    const float w[2] = {fminf(u[0] * p.cap_inv, FLT_MAX), fminf(u[1] * p.cap_inv, FLT_MAX)};
 #pragma unroll
                                     for (int e = 0; e < 4; ++e)
                                         s[r][h][e] = fmaf(-2.f * cap2, rcp_fast(exp2_fast(s[r][h][e] * w[e & 1]) + 1.f), cap2);
                                 } else {
 #pragma unroll
                                     for (int e = 0; e < 4; ++e)
-                                        s[r][h][e] = p.cap * tanh_fast(s[r][h][e] * u[e & 1] * inv) * kLog2e;
+                                        s[r][h][e] = p.cap * tanh_fast(s[r][h][e] * u[e & 1] * p.cap_inv) * kLog2e;
                                 }
                             }
                     } else if (MODS == 2) {

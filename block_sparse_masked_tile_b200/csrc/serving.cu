@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -593,6 +594,7 @@ extern "C" bsmt_status bsmt_paged_attention(const void* q, int64_t T, int64_t Hq
     p.min_share = 8;  // two tiles for each warp of a block
     p.scale = scale;
     p.cap = sa.cap;
+    p.cap_inv = static_cast<float>(std::min((sa.cap <= 64.f ? 2.0 * 1.4426950408889634 : 1.0) / sa.cap, static_cast<double>(FLT_MAX)));
     // the modes of the score program: none, soft-cap, ALiBi, soft-cap then ALiBi, ALiBi then soft-cap
     p.softcap = sa.mode == 1 || sa.mode == 3 || sa.mode == 4;
     p.alibi_first = sa.mode == 4;
