@@ -142,6 +142,7 @@ __device__ __forceinline__ bool cache_item(const CacheWriteParams& p, int64_t it
     const int64_t t0 = p.cu == nullptr ? item : __ldg(p.cu + i), t1 = p.cu == nullptr ? item + 1 : __ldg(p.cu + i + 1);
     const int seq = __ldg(p.seqs + i);
     const int64_t start = __ldg(p.starts + i);
+    if (i == 0 && t0 != 0 && p.cu != nullptr && report) set_status(p.status, BSMT_ERR_DEVICE_PRECONDITION);  // (offsets begin at 0)
     if (t0 < 0 || t1 < t0 || t1 > p.T) {
         if (report) set_status(p.status, BSMT_ERR_DEVICE_PRECONDITION);
         return false;

@@ -357,17 +357,20 @@ __global__ void __launch_bounds__(32 * PagedShape<D, NT>::kWarps, PagedShape<D, 
         describe(own);
     }
     if (tid == 0) p.heads_of_parts[blockIdx.x * 8] = 0;
-    // rows behind the last sequence belong to none: they see nothing
+    // rows behind the last sequence, or, against the conditions, in front of the first, belong to none: they see nothing
     if (p.cu != nullptr) {
-        const int64_t used = max(0, min(p.cu[p.n], static_cast<int>(p.T)));
-        if (used < p.T) {
+        const int T = static_cast<int>(p.T), used = max(0, min(p.cu[p.n], T)), front = max(0, min(p.cu[0], used));
+        if (front > 0) set_status(p.status, BSMT_ERR_DEVICE_PRECONDITION);
+        for (int part = 0; part < 2; ++part) {
+            const int64_t from = part == 0 ? used : 0, tokens = part == 0 ? T - used : front;
+            if (tokens == 0) continue;
             const int64_t stride = static_cast<int64_t>(gridDim.x) * kBlockThreads;
-            const int64_t rest = (p.T - used) * p.Hq;
-            uint4* o = reinterpret_cast<uint4*>(p.out + used * p.Hq * D);
+            const int64_t rest = tokens * p.Hq;
+            uint4* o = reinterpret_cast<uint4*>(p.out + from * p.Hq * D);
             for (int64_t x = static_cast<int64_t>(blockIdx.x) * kBlockThreads + tid; x < rest * (D / 8); x += stride)
                 o[x] = make_uint4(0, 0, 0, 0);
             for (int64_t x = static_cast<int64_t>(blockIdx.x) * kBlockThreads + tid; x < rest; x += stride)
-                p.lse[x / (p.T - used) * p.T + used + x % (p.T - used)] = -INFINITY;
+                p.lse[x / tokens * p.T + from + x % tokens] = -INFINITY;
         }
     }
     __syncthreads();

@@ -93,6 +93,10 @@ bsmt_status bsmt_rotary(const bsmt_rotary_spec* spec, int32_t dtype, int64_t B, 
  * captured into a CUDA graph once. Pages are handed out lowest first, in
  * the order of the list, so a call's result does not depend on timing.
  *
+ * Offsets (cu_seqlens) begin at 0; where they do not, the tokens in front of
+ * the first belong to no sequence, and the call reports
+ * BSMT_ERR_DEVICE_PRECONDITION.
+ *
  * Calls on one cache must not overlap in time, except reads (gather,
  * attention) with reads. head_dim is 64 or 128, page_size 16, 32, 64 or 128,
  * max_seqs at most 2^18, max_pages * page_size below 2^31 - 256
@@ -159,7 +163,8 @@ bsmt_status bsmt_cache_write(const bsmt_kv_cache* cache, int32_t layer, const in
  * NULL: from 0), for instance to run bsmt_flex_attention_fwd_packed over a
  * prompt's cached part. code * scale is exact in bf16 (while in its range).
  * Rows of entries with seqs[i] or starts[i] = -1, rows past the last offset
- * and rows of positions or pages out of range (BSMT_ERR_DEVICE_BOUNDS) are 0. */
+ * and rows of positions or pages out of range (BSMT_ERR_DEVICE_BOUNDS) are 0,
+ * and so are rows in front of the first offset. */
 bsmt_status bsmt_cache_gather(const bsmt_kv_cache* cache, int32_t layer, const int32_t* seqs, const int32_t* starts,
                               int64_t n, const int32_t* cu_seqlens, int64_t T, void* k, void* v, void* stream);
 
@@ -207,7 +212,7 @@ bsmt_status bsmt_cache_compact(const bsmt_kv_cache* cache, int32_t* live, void* 
  *         bsmt_paged_attention_workspace_bytes bytes; written and read back by
  *         the call, need not be zeroed. Calls that share one must not overlap.
  * Rows that see no key (an empty sequence, a mask that leaves nothing, an
- * entry with seqs[i] = -1, tokens at or past the last offset) get out = 0 and
+ * entry with seqs[i] = -1, tokens outside the offsets) get out = 0 and
  * lse = -inf. A page out of range counts as keys of value 0 and is reported
  * (BSMT_ERR_DEVICE_BOUNDS), as is a sequence out of range. Codes behind a
  * sequence's end and NaN codes that the mask hides do not reach the result.

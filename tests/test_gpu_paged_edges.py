@@ -132,3 +132,33 @@ def test_many_small_weights_beside_a_large_one(dim, group, far):
     tol = (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -14) * np.abs(want) + n * 2.0 ** -32 * top / total
     assert (np.abs(out.double().cpu().numpy() - want) <= tol).all(), (out[0, 0, :4], want[0, 0, :4])
     assert (np.abs(lse.double().cpu().numpy() - want_lse) <= 1e-5 * np.abs(want_lse)).all()
+
+
+def test_offsets_that_do_not_begin_at_0():
+    b = filled([40, 17], 2, 64, 32, "e4m3")
+    q, seqs, cu = queries(8, 4, 64).cuda(), ints([0, 1]), ints([3, 5, 6])
+
+    def reported():
+        with pytest.raises(RuntimeError, match="PRECONDITION"):
+            bsmt.check_device_status()
+
+    out, lse = torch.full_like(q, 7.0), torch.full((4, 8), 7.0, device="cuda")
+    bsmt.paged_attention(q, b.dev, seqs, cu, bsmt.causal(), enable_gqa=True, out=out, lse=lse)
+    reported()
+    want, want_lse = bsmt.paged_attention(q[3:6], b.dev, seqs, ints([0, 2, 3]), bsmt.causal(), enable_gqa=True)
+    assert not out[:3].any() and not out[6:].any() and torch.equal(out[3:6], want)
+    assert torch.isneginf(lse[:, :3]).all() and torch.isneginf(lse[:, 6:]).all() and torch.equal(lse[:, 3:6], want_lse)
+    bsmt.paged_attention(q, b.dev, ints([]), ints([5]), enable_gqa=True, out=out.fill_(7.0), lse=lse.fill_(7.0))  # no sequence at all
+    reported()
+    assert not out.any() and torch.isneginf(lse).all()
+    k, v = bsmt.cache_gather(b.dev, seqs, ints([0, 0]), 8, cu)
+    reported()
+    assert not k[:3].any() and k[3:6].any() and not v[6:].any()
+    # the tokens inside the offsets are written as they say
+    for T, offsets in ((8, [3, 5, 6]), (60, [50, 52, 53])):  # few tokens a sequence, and many
+        x = torch.randn((T, 2, 64), generator=torch.Generator().manual_seed(T)).bfloat16().cuda()
+        bsmt.cache_write(b.dev, seqs, ints([38, 16]), x, x, ints(offsets))
+        reported()
+        y = x.double().cpu().numpy()
+        b.ref.write(0, [0, 1], [38, 16], y, y, offsets)
+        b.equal()
