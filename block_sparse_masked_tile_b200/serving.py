@@ -23,6 +23,7 @@ from dataclasses import dataclass
 from typing import Iterable, Sequence
 
 import torch
+import torch.autograd.forward_ad as _forward_ad
 
 from . import MaskMod, ScoreMod, _check, _check_launch, _DEBUG_SYNC, _lib, _MaskSpec, _score_spec, _ScoreSpec
 
@@ -170,12 +171,31 @@ def _rotary(tensors, positions: torch.Tensor, spec: RotarySpec, inverse: bool) -
     return outs
 
 
+def _has_tangent(t: torch.Tensor) -> bool:
+    """A dual tensor of forward-mode differentiation."""
+    return _forward_ad._current_level >= 0 and _forward_ad.unpack_dual(t).tangent is not None
+
+
+def _turn(tensors, positions: torch.Tensor, spec: RotarySpec, inverse: bool) -> list:
+    """_rotary, as a differentiable op where a gradient or a tangent is to flow."""
+    if any(t.requires_grad for t in tensors) and torch.is_grad_enabled() or any(_has_tangent(t) for t in tensors):
+        return list(_RotaryFn.apply(positions, spec, inverse, *tensors))
+    return _rotary(tensors, positions, spec, inverse)
+
+
+def _rows(g: torch.Tensor) -> torch.Tensor:
+    """g with contiguous rows (a broadcast gradient, as of a sum, has stride 0 in them)."""
+    return g if g.stride(-1) == 1 or g.shape[-1] == 1 else g.contiguous()
+
+
 class _RotaryFn(torch.autograd.Function):
-    """The turn as a differentiable op; its gradient is the inverse turn."""
+    """The turn as a differentiable op. It is linear: its gradient is the inverse
+    turn, a tangent turns as its tensor does."""
 
     @staticmethod
     def forward(ctx, positions, spec, inverse, *tensors):
         ctx.save_for_backward(positions)
+        ctx.save_for_forward(positions)
         ctx.args = (spec, inverse)
         return tuple(_rotary(tensors, positions, spec, inverse))
 
@@ -185,16 +205,15 @@ class _RotaryFn(torch.autograd.Function):
         spec, inverse = ctx.args
         at = [i for i, g in enumerate(grads) if g is not None and ctx.needs_input_grad[3 + i]]
         out: list = [None] * len(grads)
-        if at:
-            # (a broadcast gradient, as of a sum, has stride 0 in its rows)
-            some = [g if g.stride(-1) == 1 or g.shape[-1] == 1 else g.contiguous() for g in (grads[i] for i in at)]
-            if torch.is_grad_enabled():  # (create_graph: the turn of the gradient is differentiable, too)
-                turned = _RotaryFn.apply(positions, spec, not inverse, *some)
-            else:
-                turned = _rotary(some, positions, spec, not inverse)
-            for i, g in zip(at, turned):
+        if at:  # (a gradient that needs one itself, as under create_graph, is turned differentiably)
+            for i, g in zip(at, _turn([_rows(grads[i]) for i in at], positions, spec, not inverse)):
                 out[i] = g
         return (None, None, None, *out)
+
+    @staticmethod
+    def jvp(ctx, _positions, _spec, _inverse, *tangents):
+        (positions,) = ctx.saved_tensors
+        return tuple(_turn([_rows(t) for t in tangents], positions, *ctx.args))
 
 
 def _rotary_args(q, k, positions, spec) -> list:
@@ -231,13 +250,11 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, spe
     strides (views of one fused projection are fine). ``positions``: int32
     [num_axes, T], [num_axes, B, T] for 4-D tensors, or [T] with one axis; any
     int32 value. Returns the turned (q, k), contiguous. Differentiable in q and
-    k. (As with any torch operation, a step with its backward pass is captured
-    into a CUDA graph while no eager graph of the same leaves is alive.)"""
+    k, in reverse and in forward mode. (As with any torch operation, a step with
+    its backward pass is captured into a CUDA graph while no eager graph of the
+    same leaves is alive.)"""
     tensors = _rotary_args(q, k, positions, spec)
-    if torch.is_grad_enabled() and any(t.requires_grad for t in tensors):
-        outs = list(_RotaryFn.apply(positions, spec, False, *tensors))
-    else:
-        outs = _rotary(tensors, positions, spec, False)
+    outs = _turn(tensors, positions, spec, False)
     return (outs[0], outs[1]) if k is not None else (outs[0], None)
 
 
