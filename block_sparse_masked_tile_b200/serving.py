@@ -260,8 +260,8 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, spe
 
 def rotary_backward(dq: torch.Tensor, dk: torch.Tensor | None, positions: torch.Tensor, spec: RotarySpec):
     """Gradients of ``rotary`` with respect to its q and k: dq and dk (may be
-    None) turned back."""
-    outs = _rotary(_rotary_args(dq, dk, positions, spec), positions, spec, True)
+    None) turned back. Differentiable as ``rotary`` is."""
+    outs = _turn(_rotary_args(dq, dk, positions, spec), positions, spec, True)
     return (outs[0], outs[1]) if dk is not None else (outs[0], None)
 
 

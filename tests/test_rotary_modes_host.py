@@ -55,3 +55,9 @@ def test_tangents_are_kept():
                 (y, _) = bsmt.rotary(fwd.make_dual(q, torch.ones(3, 2, 1, dtype=torch.float64).expand(3, 2, 10)), None, POS, SPEC)
                 assert torch.equal(fwd.unpack_dual(y).tangent, plain([torch.ones_like(q)], POS, SPEC, False)[0])
     assert bsmt.rotary(q, None, POS, SPEC)[0].grad_fn is None
+
+
+def test_rotary_backward_keeps_the_graph():
+    f = lambda dq, dk: bsmt.rotary_backward(dq, dk, POS, SPEC)  # noqa: E731
+    assert torch.autograd.gradcheck(f, (heads(2, 0, True), heads(1, 1, True)), check_forward_ad=True)
+    assert bsmt.rotary_backward(heads(2), None, POS, SPEC)[0].grad_fn is None
