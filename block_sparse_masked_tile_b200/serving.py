@@ -99,6 +99,12 @@ def _call(device: torch.device, f, *args) -> None:
             _check_launch(f(*args, torch._C._cuda_getCurrentRawStream(index)))
 
 
+def _differentiated(t: torch.Tensor) -> bool:
+    """A gradient is to flow to t, or t is a dual tensor of forward mode."""
+    return (t.requires_grad and torch.is_grad_enabled()
+            or _forward_ad._current_level >= 0 and _forward_ad.unpack_dual(t).tangent is not None)
+
+
 # ------------------------------------------------------------------ rotary
 @dataclass(frozen=True)
 class RotarySpec:
@@ -171,15 +177,11 @@ def _rotary(tensors, positions: torch.Tensor, spec: RotarySpec, inverse: bool) -
     return outs
 
 
-def _has_tangent(t: torch.Tensor) -> bool:
-    """A dual tensor of forward-mode differentiation."""
-    return _forward_ad._current_level >= 0 and _forward_ad.unpack_dual(t).tangent is not None
-
-
 def _turn(tensors, positions: torch.Tensor, spec: RotarySpec, inverse: bool) -> list:
     """_rotary, as a differentiable op where a gradient or a tangent is to flow."""
-    if any(t.requires_grad for t in tensors) and torch.is_grad_enabled() or any(_has_tangent(t) for t in tensors):
-        return list(_RotaryFn.apply(positions, spec, inverse, *tensors))
+    if any(_differentiated(t) for t in tensors):
+        outs = _RotaryFn.apply(positions, spec, inverse, *tensors)
+        return [y if _differentiated(t) else y.detach() for t, y in zip(tensors, outs)]
     return _rotary(tensors, positions, spec, inverse)
 
 
@@ -385,11 +387,14 @@ def cache_write(cache: PagedCache, seqs: torch.Tensor, starts: torch.Tensor, k: 
     other strides multiples of 8) into the pages of sequences seqs from positions
     ``starts`` on, as cache_extend returned them. ``cu_seqlens`` (int32
     [n + 1]): the sequences' tokens in the pack; None: one token each. A
-    sequence may be listed once."""
+    sequence may be listed once. No gradient flows through the cache: k and v
+    that need one are refused."""
     c, dev = _on_gpu(cache)
     n = seqs.numel()
     _, _, heads, _, dim = cache.k.shape
     for name, t in (("k", k), ("v", v)):
+        if _differentiated(t):
+            raise ValueError(f"cache_write has no backward; detach {name}")
         if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape[1:] != (heads, dim) or t.get_device() != dev.index:
             raise ValueError(f"{name} must be bfloat16 [tokens, {heads}, {dim}] on {dev}")
         if t.stride(2) != 1 and t.numel() > 0:
@@ -478,7 +483,7 @@ def paged_attention(q: torch.Tensor, cache: PagedCache, seqs: torch.Tensor, cu_s
     T, Hq, D = q.shape
     if D != cache.k.shape[4]:
         raise ValueError(f"q has head dim {D}, the cache {cache.k.shape[4]}")
-    if q.requires_grad and torch.is_grad_enabled():
+    if _differentiated(q):
         raise ValueError("paged_attention has no backward; detach q or use flex_attention_varlen")
     n = seqs.numel()
     at = _list(device, "seqs", seqs), n, _list(device, "cu_seqlens_q", cu_seqlens_q, n + 1)

@@ -61,3 +61,11 @@ def test_rotary_backward_keeps_the_graph():
     f = lambda dq, dk: bsmt.rotary_backward(dq, dk, POS, SPEC)  # noqa: E731
     assert torch.autograd.gradcheck(f, (heads(2, 0, True), heads(1, 1, True)), check_forward_ad=True)
     assert bsmt.rotary_backward(heads(2), None, POS, SPEC)[0].grad_fn is None
+
+
+def test_an_output_needs_a_gradient_where_its_tensor_does():
+    for q, k in ((heads(2, 0, True), heads(1, 1)), (heads(2), heads(1, 1, True)), (heads(2, 0, True), heads(1, 1, True))):
+        y, z = bsmt.rotary(q, k, POS, SPEC)
+        assert y.requires_grad == q.requires_grad and z.requires_grad == k.requires_grad
+        (y.sum() + z.sum()).backward()
+        assert (q.grad is not None) == q.requires_grad and (k.grad is not None) == k.requires_grad
