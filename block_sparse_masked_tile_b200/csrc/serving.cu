@@ -508,13 +508,12 @@ bsmt_status launch_paged(int dev, int nsm, bsmt::PagedParams p, const bsmt::Mask
     cfg.stream = s;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, dnf, k_map, v_map);
-    if (e != cudaSuccess) return fail(BSMT_ERR_CUDA, "paged_attention launch: %s", cudaGetErrorString(e));
+    (void)cudaLaunchKernelEx(&cfg, kern, p, dnf, k_map, v_map);
+    TRY(launched("paged_attention"));  // (reads the error and clears it, so that the next call does not find it)
     cfg.gridDim = dim3(blocks, 2 * NT);
     cfg.blockDim = dim3(32 * bsmt::kCombineWarps);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, bsmt::paged_combine_kernel<D, 8 * NT>, p);
-    if (e != cudaSuccess) return fail(BSMT_ERR_CUDA, "paged_attention combine launch: %s", cudaGetErrorString(e));
+    (void)cudaLaunchKernelEx(&cfg, bsmt::paged_combine_kernel<D, 8 * NT>, p);
     TRY(launched("paged_attention combine"));
     return BSMT_OK;
 }

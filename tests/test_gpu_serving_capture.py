@@ -103,3 +103,41 @@ print("ran")
 def test_the_first_call_of_a_process_is_captured(what):
     got = subprocess.run([sys.executable, "-c", f"WHAT = {what!r}\n" + FIRST], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert got.returncode == 0 and got.stdout.strip().endswith("ran"), got.stderr[-2000:]
+
+
+REFUSED = """
+import torch, block_sparse_masked_tile_b200 as bsmt
+i = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+c = bsmt.create_paged_cache(20, 2, 64, 4, 4, 16)
+q, seqs = torch.randn((2, 4, 64), device="cuda").bfloat16(), i(0, 2)
+out, lse = torch.empty_like(q), torch.empty((4, 2), device="cuda")
+ws = torch.empty(bsmt.paged_attention_workspace_bytes(64), dtype=torch.uint8, device="cuda")
+call = lambda: bsmt.paged_attention(q, c, seqs, enable_gqa=True, out=out, lse=lse, workspace=ws)
+call()
+bsmt.cache_free(c, seqs)
+torch.cuda.synchronize()
+side, other, g = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+
+def fails(f):
+    try:
+        f()
+    except Exception as e:
+        return str(e)
+    raise SystemExit("no error")
+
+with torch.cuda.stream(side):
+    g.capture_begin()
+    fails(torch.cuda.synchronize)  # not allowed during a capture: it ends there
+    assert "CUDA_ERROR" in fails(call)
+    with torch.cuda.stream(other):
+        bsmt.cache_free(c, seqs)  # outside the capture: as ever
+    fails(g.capture_end)
+torch.cuda.synchronize()
+bsmt.check_device_status()
+print("ran")
+"""
+
+
+def test_a_refused_launch_leaves_no_error_behind():
+    got = subprocess.run([sys.executable, "-c", REFUSED], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert got.returncode == 0 and got.stdout.strip().endswith("ran"), got.stdout[-500:] + got.stderr[-2000:]
