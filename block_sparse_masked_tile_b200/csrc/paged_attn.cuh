@@ -30,7 +30,8 @@
 //
 // Softmax in base 2 with two references for each row: m of the scores, for the
 // sum l, and mo of score + log2(v_scale), for O, so that P * v_scale, a half, stays
-// in range whatever the pages' scales are. They follow the running maxima lazily.
+// in range whatever the pages' scales are. They follow the running maxima lazily, mo
+// at a distance that lets P use a half's range to the top.
 #pragma once
 #include <cfloat>
 #include <cstdint>
@@ -73,8 +74,9 @@ struct PagedParams {
 };
 
 // Three blocks an SM with 16 KB of slots a warp; with NT = 4 (D = 64 alone) two with
-// 24 KB. (NT = 2 at D = 128, 24 sequences up to 64k with 16 rows each: 326 us in three
-// blocks of 168 registers, 363 in two of 255.) A slot holds the K or the V codes of a tile.
+// 24 KB. (NT = 2 at D = 128, 24 sequences up to 64k with 16 rows each, when it was chosen: 326 us
+// in three blocks of 168 registers, 363 in two of 255; 317 us since. The three spill some: 20 to 204
+// bytes of stores, by type and modifiers, the two none.) A slot holds the K or the V codes of a tile.
 template <int D, int NT>
 struct PagedShape {
     static constexpr int kBlocks = NT > 2 ? 2 : 3;  // of an SM

@@ -8,9 +8,9 @@
 //
 // The angle: inv_freq / 2pi is held as a 64-bit fraction of a turn. The product
 // with a 32-bit position, taken modulo 2^64, is the exact fraction of the turn
-// left after whole turns, so a far position costs no accuracy (the fraction's
-// own rounding, 2^-65 turns, times 2^31 positions is 2^-34 turns) and no 64-bit
-// floating point. Its top 32 bits give the angle to sincospif, in half turns.
+// left after whole turns, so a far position costs no accuracy (the fraction is cut
+// off below 2^-64 turns, which times 2^31 positions is 2^-33 turns; an inv_freq of
+// whole turns keeps as many bits less of it) and no 64-bit floating point. Its top 32 bits give the angle to sincospif, in half turns.
 //
 // Bound by HBM: x is read once and written once. A thread keeps the sines of
 // its eight pairs of one token in registers and goes over heads of q and k with

@@ -504,7 +504,8 @@ const char* bsmt_last_error(void);
  * last check. */
 bsmt_status bsmt_check_device_status(void* stream);
 
-/* ABI version: (major << 16) | minor. */
+/* ABI version: (major << 16) | minor. What only adds to it, as bsmt_serving.h and
+ * its status code did, leaves the number as it is. */
 int32_t bsmt_version(void);
 
 #ifdef __cplusplus

@@ -217,8 +217,9 @@ bsmt_status bsmt_cache_compact(const bsmt_kv_cache* cache, int32_t* live, void* 
  * (BSMT_ERR_DEVICE_BOUNDS), as is a sequence out of range. Codes behind a
  * sequence's end and NaN codes that the mask hides do not reach the result.
  * V scales may differ by up to 2^100 within a sequence. Made for few queries
- * a sequence (rows are taken 16 or 32 at a time, and each such tile reads the
- * keys again, from L2 mostly); the result does not depend on timing. */
+ * a sequence (a row is one query of one head of a kv head's group; rows are
+ * taken 8 or 16 at a time, with a head_dim of 64 also 32, and each such tile
+ * reads the keys again, from L2 mostly); the result does not depend on timing. */
 bsmt_status bsmt_paged_attention_workspace_bytes(int64_t D, int64_t* bytes);
 bsmt_status bsmt_paged_attention(const void* q, int64_t T, int64_t Hq, const bsmt_kv_cache* cache, int32_t layer,
                                  const int32_t* seqs, int64_t n, const int32_t* cu_seqlens_q,
